@@ -376,6 +376,181 @@ ssm_status ssm_conv1d_silu(const void *x, void *u, const float *w, const float *
                            int64_t Dn, int64_t L, int32_t K, int32_t in_dtype, int32_t out_dtype,
                            void *stream);
 
+/*
+ * Gated linear recurrence: per batch element and channel one decaying state, whose decay and input
+ * are gated by the token (the real-gated linear recurrent unit):
+ *
+ *   r_t = sigmoid(r~_t + r_bias[d]),  g_t = sigmoid(i~_t + i_bias[d])
+ *   a_t = exp(-c softplus(lam[d]) r_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) g_t x_t,   h_{-1} = h0 or 0,   out_t = h_t
+ *
+ * x, r~ and i~ are given (the gates' projections are the caller's). State and sums are fp32. A layer
+ * runs the causal conv of this library in front of it.
+ *  - reset marks steps that start a new sequence (packed rows): h_{t-1} counts as 0 there, and
+ *    nothing of an earlier sequence reaches a later one, NaN and infinity included, in either direction.
+ *  - lengths gives each batch element's live steps, 0 .. L (larger values count as L, negative ones as 0): out and the gradients are 0 behind
+ *    them, whatever the inputs hold there, and h_last is the state after the last live step (h0
+ *    with none).
+ *  - chunk_states is opaque: what ssm_lru_bwd needs of a forward over the same Bt, Dn and L.
+ */
+
+/* Saved states per channel for a sequence of length L: the last axis of chunk_states. */
+int64_t ssm_lru_num_states(int64_t L);
+
+typedef struct ssm_lru_args {
+  const void *x;         /* device (Bt, Dn, L) in_dtype */
+  const void *r;         /* device (Bt, Dn, L) in_dtype: r~, the decay gate before its sigmoid */
+  const void *i;         /* device (Bt, Dn, L) in_dtype: i~, the input gate before its sigmoid */
+  const float *lam;      /* device [Dn] */
+  const float *r_bias;   /* device [Dn] or NULL (= 0) */
+  const float *i_bias;   /* device [Dn] or NULL (= 0) */
+  const float *h0;       /* device (Bt, Dn) fp32 or NULL (= 0): the state before step 0 */
+  const uint8_t *reset;  /* device (Bt, L) or NULL: non-zero where a sequence starts */
+  const int32_t *lengths;/* device [Bt] or NULL (= L) */
+  void *out;             /* device (Bt, Dn, L) out_dtype, not one of the inputs (ignored by ssm_lru_bwd) */
+  float *chunk_states;   /* device (Bt, Dn, ssm_lru_num_states(L)) fp32 or NULL */
+  float *h_last;         /* device (Bt, Dn) fp32 or NULL: the state after the last live step */
+  int64_t Bt, Dn, L;
+  float c;               /* > 0 and finite */
+  int32_t in_dtype;      /* ssm_dtype of x, r, i (and dout) */
+  int32_t out_dtype;     /* ssm_dtype of out */
+} ssm_lru_args;
+
+/* Errors: SSM_ERR_NULL (x, r, i, lam or out NULL), SSM_ERR_SHAPE, SSM_ERR_ALIGN, SSM_ERR_DTYPE,
+ * SSM_ERR_UNSUPPORTED (c), SSM_ERR_CUDA. L = 0: h_last = h0 or 0. */
+ssm_status ssm_lru_fwd(const ssm_lru_args *args, void *stream);
+
+typedef struct ssm_lru_bwd_args {
+  ssm_lru_args fwd;        /* forward inputs; out and h_last are ignored; chunk_states: saved by ssm_lru_fwd,
+                              or NULL: recomputed into the workspace */
+  const void *dout;        /* device (Bt, Dn, L) in_dtype */
+  const float *dh_last;    /* device (Bt, Dn) fp32 or NULL: gradient arriving at h_last */
+  void *dx, *dr, *di;      /* device (Bt, Dn, L) grad_dtype, each or NULL: w.r.t. x, r~, i~ */
+  float *dlam;             /* device [Dn] or NULL */
+  float *dr_bias;          /* device [Dn] or NULL */
+  float *di_bias;          /* device [Dn] or NULL */
+  float *dh0;              /* device (Bt, Dn) or NULL */
+  int32_t grad_dtype;      /* ssm_dtype of dx, dr, di */
+  void *workspace;         /* device scratch of ssm_lru_bwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} ssm_lru_bwd_args;
+
+/* Scratch bytes of ssm_lru_bwd: the states when none are given, the per-row parameter sums when Bt > 1 and a parameter gradient is wanted. 0 for an empty or
+ * invalid problem. */
+size_t ssm_lru_bwd_workspace_size(const ssm_lru_bwd_args *args);
+
+/* The vector-Jacobian product of ssm_lru_fwd: outputs overwritten, deterministic (sums in a fixed
+ * order, no atomics). Errors as ssm_lru_fwd, plus SSM_ERR_WORKSPACE. An empty problem (Bt = 0 or L = 0) writes zeros to the parameter
+ * gradients and dh0 = dh_last or 0. */
+ssm_status ssm_lru_bwd(const ssm_lru_bwd_args *args, void *stream);
+
+/* One token: h (Bt, Dn) fp32 is read and overwritten in place; the arithmetic of ssm_lru_fwd with L = 1. */
+typedef struct ssm_lru_step_args {
+  const void *x, *r, *i;   /* device (Bt, Dn) in_dtype */
+  const float *lam;        /* device [Dn] */
+  const float *r_bias;     /* device [Dn] or NULL */
+  const float *i_bias;     /* device [Dn] or NULL */
+  float *h;                /* device (Bt, Dn) fp32 */
+  void *out;               /* device (Bt, Dn) out_dtype */
+  int64_t Bt, Dn;
+  float c;
+  int32_t in_dtype, out_dtype;
+} ssm_lru_step_args;
+
+ssm_status ssm_lru_step(const ssm_lru_step_args *args, void *stream);
+
+/*
+ * Normalisation of queries and keys over each head, and rotation by position, in one pass. In this
+ * library's terms C is the query and B the key of the scan (one head of N elements, time
+ * innermost) and of the state-space dual (one head, elements innermost); with a real decay, C and B
+ * turned by an angle proportional to the position make the state's decay complex.
+ *
+ * Per token t and head, v the D elements of q or k:
+ *   n   = v / sqrt(mean(v^2) + eps) * weight        (norm = 1; n = v with norm = 0)
+ *   rotation of the first `rot` elements, in pairs j = 0 .. rot/2 - 1: (j, j + rot/2), or
+ *   (2 j, 2 j + 1) with interleaved = 1:
+ *     (n_p, n_q) -> rot_scale (n_p cos - n_q sin, n_q cos + n_p sin),  angle = position * inv_freq[j]
+ *   the elements from rot on pass as they are.
+ * The angle and its reduction are computed in 64 bits, so positions up to 2^53 keep theirs.
+ *
+ * Element (b, t, h, e) of a tensor lies at b sb + h sh + t sr + e (layout SSM_QK_STATE_LAST), or
+ * b sb + h sh + e sr + t (SSM_QK_TIME_LAST); strides count elements. Inputs may have any strides
+ * (0 repeats); outputs must not overlap themselves. q_out may be q itself (same pointer, strides and
+ * dtype), and k_out k; they may not overlap otherwise. Hq or Hk may be 0 (its pointers are ignored).
+ */
+typedef enum ssm_qk_layout { SSM_QK_STATE_LAST = 0, SSM_QK_TIME_LAST = 1 } ssm_qk_layout;
+
+typedef struct ssm_qk_args {
+  const void *q;           /* device in_dtype */
+  const void *k;           /* device in_dtype */
+  const float *q_weight;   /* device [D] or NULL (= 1); only with norm */
+  const float *k_weight;   /* device [D] or NULL (= 1); only with norm */
+  const void *inv_freq;    /* device [rot / 2], fp32 or (freq_f64) fp64; may be NULL with rot = 0 */
+  const void *positions;   /* device (Bt, L), int32 or (pos_i64) int64, or NULL: step t has position pos0 + t */
+  void *q_out, *k_out;     /* device out_dtype */
+  int64_t q_sb, q_sh, q_sr;
+  int64_t k_sb, k_sh, k_sr;
+  int64_t q_out_sb, q_out_sh, q_out_sr;
+  int64_t k_out_sb, k_out_sh, k_out_sr;
+  int64_t Bt, L, Hq, Hk, D;
+  int64_t rot;             /* rotated elements: even, 0 .. D */
+  int64_t pos0;
+  float eps, rot_scale;    /* eps >= 0 */
+  int32_t layout;          /* ssm_qk_layout */
+  int32_t norm, interleaved, freq_f64, pos_i64;
+  int32_t in_dtype, out_dtype;
+} ssm_qk_args;
+
+/* Errors: SSM_ERR_NULL, SSM_ERR_SHAPE (negative sizes, D = 0, odd or too large rot, an output that
+ * overlaps itself), SSM_ERR_ALIGN, SSM_ERR_DTYPE, SSM_ERR_UNSUPPORTED (D > 512, an unknown layout, a negative or
+ * NaN eps, a weight without norm), SSM_ERR_CUDA. Bt = 0, L = 0 or no heads: nothing to do. */
+ssm_status ssm_qk_norm_rope_fwd(const ssm_qk_args *args, void *stream);
+
+typedef struct ssm_qk_bwd_args {
+  ssm_qk_args fwd;         /* forward inputs; q_out, k_out and out_dtype are ignored. Without norm q and k are not read
+                              (NULL is fine). Their _out strides are those of dq_out / dk_out. */
+  const void *dq_out;      /* device dout_dtype: gradient of q_out, with strides q_out_s* */
+  const void *dk_out;
+  void *dq, *dk;           /* device grad_dtype, or NULL: not wanted; may be dq_out (dk_out)
+                              itself (same pointer, strides and dtype) */
+  int64_t dq_sb, dq_sh, dq_sr;
+  int64_t dk_sb, dk_sh, dk_sr;
+  float *dq_weight;        /* device [D] or NULL; only with norm */
+  float *dk_weight;
+  int32_t dout_dtype, grad_dtype;
+  void *workspace;         /* device scratch of ssm_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} ssm_qk_bwd_args;
+
+/* Scratch of ssm_qk_norm_rope_bwd: the per-CTA weight sums; 0 when no weight gradient is wanted. */
+size_t ssm_qk_norm_rope_bwd_workspace_size(const ssm_qk_bwd_args *args);
+
+/* Outputs overwritten, deterministic. Errors as the forward's, plus SSM_ERR_WORKSPACE. An empty problem writes zeros to
+ * the weight gradients. */
+ssm_status ssm_qk_norm_rope_bwd(const ssm_qk_bwd_args *args, void *stream);
+
+/*
+ * One token of the state-space dual (ssm_ssd_fwd's recurrence with L = 1): h is read and overwritten,
+ *   h = a h + beta B x^T,  y = h^T C + D x    per head. bf16 or fp32 inputs, P and N up to 256.
+ */
+typedef struct ssm_ssd_step_args {
+  const void *x;           /* device (Bt, H, P) in_dtype */
+  const void *dt;          /* device (Bt, H) in_dtype */
+  const float *dt_bias;    /* device [H] or NULL (= 0) */
+  const float *A_log;      /* device [H] */
+  const void *B;           /* device (Bt, N) in_dtype */
+  const void *C;           /* device (Bt, N) in_dtype */
+  const float *D;          /* device [H] or NULL (= 0) */
+  float *h;                /* device (Bt, H, N, P) fp32 */
+  void *out;               /* device (Bt, H, P) out_dtype */
+  int64_t Bt, H, P, N;
+  int32_t in_dtype, out_dtype, delta_softplus, discretization;
+} ssm_ssd_step_args;
+
+/* Errors: SSM_ERR_NULL, SSM_ERR_SHAPE, SSM_ERR_ALIGN, SSM_ERR_DTYPE, SSM_ERR_UNSUPPORTED (P or N > 256, an unknown
+ * discretization), SSM_ERR_CUDA. Bt = 0 is a no-op. */
+ssm_status ssm_ssd_step(const ssm_ssd_step_args *args, void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *ssm_status_string(ssm_status s);
 

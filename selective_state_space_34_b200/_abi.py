@@ -12,6 +12,7 @@ SSM_F32, SSM_BF16 = 0, 1
 SSM_ZOH, SSM_EULER = 0, 1
 SSM_SCAN_LANES, SSM_SCAN_CHUNKED = 0, 1
 SSM_SSD_AUTO, SSM_SSD_THREE_PASS, SSM_SSD_FUSED = 0, 1, 2
+SSM_QK_STATE_LAST, SSM_QK_TIME_LAST = 0, 1
 SSM_STATE_CHUNK = 16
 SSM_NOALLOC_SCRATCH_BYTES = 72 << 20
 SSM_ERR_TIMEOUT = 8
@@ -79,6 +80,46 @@ class SsdArgs(ctypes.Structure):
     ]
 
 
+_P, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+def _fields(*groups):
+    """(names, type) groups as a ctypes field list."""
+    return [(n, t) for names, t in groups for n in names.split()]
+
+
+class LruArgs(ctypes.Structure):
+    _fields_ = _fields(("x r i lam r_bias i_bias h0 reset lengths out chunk_states h_last", _P), ("Bt Dn L", _I64),
+                       ("c", _F32), ("in_dtype out_dtype", _I32))
+
+
+class LruBwdArgs(ctypes.Structure):
+    _fields_ = _fields(("fwd", LruArgs), ("dout dh_last dx dr di dlam dr_bias di_bias dh0", _P), ("grad_dtype", _I32),
+                       ("workspace", _P), ("workspace_bytes", ctypes.c_size_t))
+
+
+class LruStepArgs(ctypes.Structure):
+    _fields_ = _fields(("x r i lam r_bias i_bias h out", _P), ("Bt Dn", _I64), ("c", _F32), ("in_dtype out_dtype", _I32))
+
+
+class QkArgs(ctypes.Structure):
+    _fields_ = _fields(("q k q_weight k_weight inv_freq positions q_out k_out", _P),
+                       ("q_sb q_sh q_sr k_sb k_sh k_sr q_out_sb q_out_sh q_out_sr k_out_sb k_out_sh k_out_sr", _I64),
+                       ("Bt L Hq Hk D rot pos0", _I64), ("eps rot_scale", _F32),
+                       ("layout norm interleaved freq_f64 pos_i64 in_dtype out_dtype", _I32))
+
+
+class QkBwdArgs(ctypes.Structure):
+    _fields_ = _fields(("fwd", QkArgs), ("dq_out dk_out dq dk", _P), ("dq_sb dq_sh dq_sr dk_sb dk_sh dk_sr", _I64),
+                       ("dq_weight dk_weight", _P), ("dout_dtype grad_dtype", _I32), ("workspace", _P),
+                       ("workspace_bytes", ctypes.c_size_t))
+
+
+class SsdStepArgs(ctypes.Structure):
+    _fields_ = _fields(("x dt dt_bias A_log B C D h out", _P), ("Bt H P N", _I64),
+                       ("in_dtype out_dtype delta_softplus discretization", _I32))
+
+
 # (name, restype, argtypes) of every exported function in include/ssm_scan.h
 SIGNATURES = [
     ("ssm_num_state_chunks", ctypes.c_int64, [ctypes.c_int64]),
@@ -92,6 +133,15 @@ SIGNATURES = [
     ("ssm_ssd_workspace_size", ctypes.c_size_t, [ctypes.POINTER(SsdArgs)]),
     ("ssm_ssd_fwd", ctypes.c_int, [ctypes.POINTER(SsdArgs), ctypes.c_void_p]),
     ("ssm_ssd_check", ctypes.c_int, [ctypes.POINTER(SsdArgs), ctypes.c_void_p]),
+    ("ssm_ssd_step", ctypes.c_int, [ctypes.POINTER(SsdStepArgs), ctypes.c_void_p]),
+    ("ssm_lru_num_states", ctypes.c_int64, [ctypes.c_int64]),
+    ("ssm_lru_fwd", ctypes.c_int, [ctypes.POINTER(LruArgs), ctypes.c_void_p]),
+    ("ssm_lru_bwd_workspace_size", ctypes.c_size_t, [ctypes.POINTER(LruBwdArgs)]),
+    ("ssm_lru_bwd", ctypes.c_int, [ctypes.POINTER(LruBwdArgs), ctypes.c_void_p]),
+    ("ssm_lru_step", ctypes.c_int, [ctypes.POINTER(LruStepArgs), ctypes.c_void_p]),
+    ("ssm_qk_norm_rope_fwd", ctypes.c_int, [ctypes.POINTER(QkArgs), ctypes.c_void_p]),
+    ("ssm_qk_norm_rope_bwd_workspace_size", ctypes.c_size_t, [ctypes.POINTER(QkBwdArgs)]),
+    ("ssm_qk_norm_rope_bwd", ctypes.c_int, [ctypes.POINTER(QkBwdArgs), ctypes.c_void_p]),
     ("ssm_wait_selftest", ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
     ("ssm_conv1d_silu", ctypes.c_int,
      [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,

@@ -5,21 +5,11 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/ssm_scan.h"
+#include "ssm_api_util.h"
 #include "ssm_internal.h"
 
 namespace {
-
-// An NVTX range named after the entry point around its host work and launches, so a profiler's
-// timeline groups each call's kernels under the API call that issued them. Header-only NVTX v3:
-// without an attached tool a push or pop is one predictable branch.
-struct NvtxRange {
-  explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
-#define SSM_RANGE(name) NvtxRange ssm_nvtx_range_(name)
 
 thread_local int g_last_cuda_error = 0;
 
@@ -36,17 +26,6 @@ int record_cuda_error_code(cudaError_t e) { return (int)cuda_status(e); }
 }  // namespace ssm
 
 namespace {
-
-size_t dtype_size(int32_t dt) { return dt == SSM_BF16 ? 2 : 4; }
-bool dtype_ok(int32_t dt) { return dt == SSM_F32 || dt == SSM_BF16; }
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t *out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > INT64_MAX / a) return false;
-  *out = a * b;
-  return true;
-}
 
 // Shape, dtype and pointer checks shared by forward and backward. Sets *empty for Bt = 0 or L = 0.
 ssm_status check_fwd(const ssm_fwd_args *a, bool need_out, bool *empty) {

@@ -132,6 +132,81 @@ struct BwdParams {
                                // before it, added into the previous segment's dx afterwards
 };
 
+// Gated linear recurrence (ssm_lru.cu).
+struct LruParams {
+  const void *x, *r, *i;             // (Bt, Dn, L)
+  const float *lam, *r_bias, *i_bias;  // [Dn]
+  const float *h0;                   // (Bt, Dn) or null
+  const uint8_t *reset;              // (Bt, L) or null: non-zero where a sequence starts
+  const int32_t *lengths;            // [Bt] or null: live steps of each row
+  void *out;                         // (Bt, Dn, L), or null: only the states are wanted
+  float *states;                     // (Bt, Dn, n_states) or null: the state that enters every chunk
+  float *h_last;                     // (Bt, Dn) or null
+  int64_t Bt, Dn, L, n_states;
+  float c;
+  int vec, vec_out;                  // inputs (out) on 16-byte boundaries
+};
+struct LruBwdParams {
+  LruParams f;                       // f.states: the saved states
+  const void *dout;
+  void *dx, *dr, *di;                // (Bt, Dn, L) or null
+  const float *dh_last;              // (Bt, Dn) or null
+  float *dh0;                        // (Bt, Dn) or null
+  float *p_dlam, *p_dr, *p_di;       // (Bt, Dn) per-row sums (the outputs themselves with Bt = 1), or null
+  float *dlam, *dr_bias, *di_bias;   // [Dn] or null
+  int vec_grad;
+};
+struct LruStepParams {
+  const void *x, *r, *i;             // (Bt, Dn)
+  const float *lam, *r_bias, *i_bias;
+  float *h;                          // (Bt, Dn), updated
+  void *out;
+  int64_t Bt, Dn;
+  float c;
+  int vec;                           // Dn a multiple of 4, every pointer on a 4-element boundary
+};
+cudaError_t launch_lru_fwd(const LruParams &p, int in_bf16, int out_bf16, cudaStream_t stream);
+cudaError_t launch_lru_bwd(const LruBwdParams &p, int in_bf16, int grad_bf16, cudaStream_t stream);
+cudaError_t launch_lru_step(const LruStepParams &p, int in_bf16, int out_bf16, cudaStream_t stream);
+
+// Normalisation and rotation of queries and keys (ssm_qk.cu). Side 0: queries, side 1: keys.
+struct QkTensor {
+  void *p;               // read only where it is an input
+  int64_t sb, sh, sr;    // strides in elements: batch, head, row (a token, or a component with time_last)
+  int bf16;
+};
+struct QkParams {
+  QkTensor in[2], out[2];    // backward: out is the gradient of in
+  QkTensor dout[2];          // backward only
+  const float *w[2];         // [D] or null (= 1)
+  float *dw[2];              // [D] or null
+  float *part;               // (blocks, D) per-block sums of dw
+  const void *inv_freq;      // [rot / 2]
+  const void *pos;           // (Bt, L) or null
+  int64_t pos0;              // position of step 0 without pos
+  int64_t Bt, L;
+  int H[2], D, rot;
+  int freq_f64, pos_i64, interleaved, norm, time_last;
+  int vec;                   // 16-byte accesses: see qk_vec_ok in ssm_api_ops.cu
+  float eps, rot_scale, inv_D;  // inv_D = 1 / D
+};
+cudaError_t launch_qk_fwd(const QkParams &p, int in_bf16, cudaStream_t stream);
+cudaError_t launch_qk_bwd(const QkParams &p, int in_bf16, cudaStream_t stream);
+// Bytes of QkParams::part for a backward that wants dw.
+size_t qk_bwd_workspace_bytes(const QkParams &p);
+constexpr int kQkMaxDim = 512;  // largest head size
+
+// One token of the state-space dual (ssm_ssd_step.cu).
+struct SsdStepParams {
+  const void *x, *dt, *B, *C;        // (Bt, H, P), (Bt, H), (Bt, N), (Bt, N)
+  const float *dt_bias, *A_log, *D;  // [H]
+  float *h;                          // (Bt, H, N, P), updated
+  void *out;                         // (Bt, H, P)
+  int64_t Bt, H, P, N;
+  int delta_softplus, euler, vec;    // vec: P a multiple of 4 and h on a 16-byte boundary
+};
+cudaError_t launch_ssd_step(const SsdStepParams &p, int in_bf16, int out_bf16, cudaStream_t stream);
+
 // Maps a CUDA error to the C ABI's status and records it for ssm_last_cuda_error() on this host
 // thread (SSM_OK for cudaSuccess). The status type is the ABI's, passed as int here.
 int record_cuda_error_code(cudaError_t e);

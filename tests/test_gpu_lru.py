@@ -1,0 +1,294 @@
+"""The gated linear recurrence on the GPU against the float64 recurrence, with derived bounds (layer_refs)."""
+import pytest
+import torch
+
+import layer_refs as ref
+import selective_state_space_34_b200 as ssm
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def inputs(Bt, Dn, L, dtype, seed=0, step=False):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s, std=1.0: torch.randn(s, generator=g) * std  # noqa: E731
+    shape = (Bt, Dn) if step else (Bt, Dn, L)
+    t = {k: n(*shape).clamp(-7, 7).to(dtype).cuda() for k in ("x", "r", "i", "dout")}
+    decay = torch.rand(Dn, generator=g) * 0.099 + 0.9
+    decay[:: 3] = torch.rand(decay[:: 3].shape, generator=g) * 0.9 + 0.05  # fast channels among slow ones
+    t["lam"] = torch.log(torch.expm1(-torch.log(decay) / 8.0)).cuda()
+    t["r_bias"], t["i_bias"] = n(Dn, std=0.3).cuda(), n(Dn, std=0.3).cuda()
+    t["h0"], t["dh_last"] = n(Bt, Dn).cuda(), n(Bt, Dn).cuda()
+    t["reset"] = (torch.rand(Bt, L, generator=g) < 0.03).cuda()
+    t["lengths"] = torch.randint(0, L + 1, (Bt,), generator=g, dtype=torch.int32).cuda()
+    return t
+
+
+def options(t, names):
+    return {k: t[k] for k in names}
+
+
+def compare(got, want, half, grad_half=None):
+    for k, v in got.items():
+        if k == "chunk_states":
+            continue
+        value, bound = want[k]
+        h = half if k == "out" else grad_half if k in ("dx", "dr", "di") else ref.EPS
+        ref.check(k, v, value, bound + h * (value.abs() + bound) + 1e-37)
+
+
+FULL = ("r_bias", "i_bias", "h0")
+CASES = [
+    # Bt, Dn, L: one token; inside a group; a group; around a chunk; rows off the 16-byte boundary
+    (1, 1, 1), (2, 3, 5), (1, 4, 8), (2, 5, 255), (1, 2, 256), (3, 3, 257), (2, 6, 513), (2, 37, 777), (1, 3, 2049),
+    (1, 2, 5000), (2, 9, 1024),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("Bt,Dn,L", CASES)
+def test_forward_and_backward(Bt, Dn, L, dtype):
+    t = inputs(Bt, Dn, L, dtype, seed=L)
+    kw = options(t, FULL)
+    args = (t["x"], t["r"], t["i"], t["lam"])
+    want = ref.lru(*args, dout=t["dout"], dh_last=t["dh_last"], **kw)
+    f = ssm.ssm_lru_fwd(*args, save_states=True, return_state=True, **kw)
+    assert f["out"].dtype == dtype
+    compare(f, want, ref.HALF[dtype])
+    for grad in (F32, BF):
+        g = ssm.ssm_lru_bwd(t["dout"], *args, chunk_states=f["chunk_states"], dh_last=t["dh_last"], grad_dtype=grad, **kw)
+        assert g["dx"].dtype == grad and set(g) == {"dx", "dr", "di", "dlam", "dr_bias", "di_bias", "dh0"}
+        compare(g, want, None, ref.HALF[grad])
+    again = ssm.ssm_lru_bwd(t["dout"], *args, dh_last=t["dh_last"], grad_dtype=BF, **kw)  # states recomputed
+    assert all(torch.equal(again[k], g[k]) for k in g)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(F32, BF), (BF, F32)])
+def test_output_types_and_no_options(dtype, out_dtype):
+    t = inputs(2, 7, 300, dtype)
+    args = (t["x"], t["r"], t["i"], t["lam"])
+    out = ssm.ssm_lru_fwd(*args, out_dtype=out_dtype, c=3.0)
+    assert out.dtype == out_dtype
+    want = ref.lru(*args, c=3.0, dout=t["dout"])
+    compare({"out": out}, want, ref.HALF[out_dtype])
+    g = ssm.ssm_lru_bwd(t["dout"], *args, c=3.0)
+    assert set(g) == {"dx", "dr", "di", "dlam"}
+    compare(g, want, None, ref.EPS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("Bt,Dn,L", [(3, 5, 40), (2, 6, 700), (3, 3, 2050)])
+def test_packed_and_padded(Bt, Dn, L, dtype):
+    t = inputs(Bt, Dn, L, dtype, seed=3)
+    t["reset"][0, : min(L, 30)] = True  # sequences of one token
+    t["reset"][-1, 0] = True             # h0 is cut off
+    t["lengths"][0] = 0                  # a row without live steps
+    t["lengths"][-1] = L
+    kw = options(t, FULL + ("reset", "lengths"))
+    args = (t["x"], t["r"], t["i"], t["lam"])
+    want = ref.lru(*args, dout=t["dout"], dh_last=t["dh_last"], **kw)
+    behind = torch.arange(L, device="cuda") >= t["lengths"][:, None]
+    for k in ("x", "r", "i", "dout"):  # what stands behind a length is never used
+        t[k].masked_fill_(behind[:, None, :], float("nan"))
+    f = ssm.ssm_lru_fwd(*args, save_states=True, return_state=True, **kw)
+    compare(f, want, ref.HALF[dtype])
+    g = ssm.ssm_lru_bwd(t["dout"], *args, chunk_states=f["chunk_states"], dh_last=t["dh_last"], **kw)
+    compare(g, want, None, ref.EPS)
+    as_bytes = dict(kw, reset=t["reset"].to(torch.uint8) * 7)
+    assert torch.equal(ssm.ssm_lru_fwd(*args, **as_bytes), f["out"])
+    over = dict(kw, lengths=torch.where(t["lengths"] == L, L + 100, t["lengths"]).to(torch.int32))
+    over["lengths"][0] = -5
+    assert torch.equal(ssm.ssm_lru_fwd(*args, **over), f["out"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("L,cut", [(64, 21), (900, 300), (4096, 1500)])
+def test_nothing_crosses_a_reset(L, cut, bad, dtype):
+    """NaN or infinity in one of two packed sequences leaves the other's results as they are, both ways."""
+    t = inputs(1, 3, L, dtype, seed=11)
+    reset = torch.zeros(1, L, dtype=torch.bool, device="cuda")
+    reset[0, cut] = True
+    args = (t["x"], t["r"], t["i"], t["lam"])
+
+    def both(x, r, dout):
+        f = ssm.ssm_lru_fwd(x, r, *args[2:], reset=reset, save_states=True)
+        g = ssm.ssm_lru_bwd(dout, x, r, *args[2:], reset=reset, chunk_states=f["chunk_states"])
+        return f["out"], g
+
+    out, g = both(t["x"], t["r"], t["dout"])
+    x, r, d = t["x"].clone(), t["r"].clone(), t["dout"].clone()
+    x[..., cut - 3] = r[..., cut - 2] = d[..., cut - 4] = bad
+    out1, g1 = both(x, r, d)
+    assert torch.equal(out1[..., cut:], out[..., cut:])
+    assert all(torch.equal(g1[k][..., cut:], g[k][..., cut:]) for k in ("dx", "dr", "di"))
+    x, r, d = t["x"].clone(), t["r"].clone(), t["dout"].clone()
+    x[..., cut + 2] = r[..., cut + 1] = d[..., cut] = bad
+    out2, g2 = both(x, r, d)
+    assert torch.equal(out2[..., :cut], out[..., :cut])
+    assert all(torch.equal(g2[k][..., :cut], g[k][..., :cut]) for k in ("dx", "dr", "di"))
+
+
+def test_nan_reaches_its_own_sequence():
+    for k in ("x", "r", "i"):
+        t = inputs(1, 2, 40, BF)
+        t[k][0, 0, 7] = float("nan")
+        out = ssm.ssm_lru_fwd(t["x"], t["r"], t["i"], t["lam"])
+        assert bool(out[0, 0, 7:].isnan().all()) and bool(out[0, 0, :7].isfinite().all())
+        assert bool(out[0, 1].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_extreme_decays(dtype):
+    """Decays of 1 (softplus underflows), of 0, and gates that saturate: finite, and the formula's values."""
+    L = 300
+    t = inputs(1, 6, L, dtype, seed=4)
+    t["lam"] = torch.tensor([-200.0, -60.0, -20.0, 5.0, 60.0, 300.0]).cuda()
+    for k, v in (("r", -7.0), ("i", 7.0)):
+        t[k][..., :100] = v
+    kw = options(t, ("h0",))
+    args = (t["x"], t["r"], t["i"], t["lam"])
+    f = ssm.ssm_lru_fwd(*args, save_states=True, return_state=True, **kw)
+    g = ssm.ssm_lru_bwd(t["dout"], *args, chunk_states=f["chunk_states"], **kw)
+    assert all(bool(v.isfinite().all()) for v in list(f.values()) + list(g.values()))
+    assert torch.equal(f["h_last"][0, 0], t["h0"][0, 0])  # a = 1, b = 0
+    # decays of nearly 0: h_t is b_t (the log decay below -40 * the least open gate)
+    want = ref.lru(*args, dout=t["dout"], **kw)
+    value, bound = want["out"]
+    ref.check("out", f["out"][:, 2:4], value[:, 2:4], (bound + ref.HALF[dtype] * (value.abs() + bound))[:, 2:4])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_chained_chunks_equal_one_call(dtype):
+    t = inputs(2, 5, 640, dtype)
+    rest = (t["lam"], t["r_bias"], t["i_bias"])
+    whole = ssm.ssm_lru_fwd(t["x"], t["r"], t["i"], *rest, h0=t["h0"], return_state=True)
+    want = ref.lru(t["x"], t["r"], t["i"], *rest, h0=t["h0"])
+    h, outs = t["h0"], []
+    for lo, hi in ((0, 256), (256, 300), (300, 301), (301, 640)):
+        part = [t[k][..., lo:hi].contiguous() for k in ("x", "r", "i")]
+        f = ssm.ssm_lru_fwd(*part, *rest, h0=h, return_state=True)
+        outs.append(f["out"])
+        h = f["h_last"]
+    compare({"out": torch.cat(outs, -1), "h_last": h}, want, ref.HALF[dtype])
+    compare({"out": whole["out"], "h_last": whole["h_last"]}, want, ref.HALF[dtype])
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(F32, F32), (BF, BF), (BF, F32)])
+@pytest.mark.parametrize("Bt,Dn", [(1, 1), (3, 7), (5, 128), (64, 1000)])
+def test_step(Bt, Dn, dtype, out_dtype):
+    t = inputs(Bt, Dn, 1, dtype, step=True)
+    h = t["h0"].clone()
+    out = ssm.ssm_lru_step(t["x"], t["r"], t["i"], t["lam"], h, t["r_bias"], t["i_bias"], out_dtype=out_dtype)
+    three = (t[k][..., None] for k in ("x", "r", "i"))
+    want = ref.lru(*three, t["lam"], t["r_bias"], t["i_bias"], h0=t["h0"])
+    compare({"h_last": h}, want, None)
+    compare({"out": out[..., None]}, want, ref.HALF[out_dtype])
+
+
+def test_views_off_the_vector_boundary():
+    """The same values one element off the 16-byte boundary take the element path and give the same bits."""
+    t = inputs(2, 5, 517, BF)
+
+    def off(v):
+        w = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")[1:].view(v.shape)
+        return w.copy_(v)
+
+    args = [t[k] for k in ("x", "r", "i")]
+    f = ssm.ssm_lru_fwd(*args, t["lam"], h0=t["h0"], save_states=True)
+    u = ssm.ssm_lru_fwd(*(off(v) for v in args), off(t["lam"]), h0=off(t["h0"]), out=off(torch.zeros_like(t["x"])),
+                        save_states=True)
+    assert torch.equal(f["out"], u["out"]) and torch.equal(f["chunk_states"][..., 0], u["chunk_states"][..., 0])
+    g = ssm.ssm_lru_bwd(t["dout"], *args, t["lam"], h0=t["h0"], chunk_states=f["chunk_states"])
+    v = ssm.ssm_lru_bwd(off(t["dout"]), *(off(v) for v in args), t["lam"], h0=t["h0"], chunk_states=f["chunk_states"])
+    assert all(torch.equal(g[k], v[k]) for k in g)
+    s = inputs(3, 8, 1, BF, step=True)
+    h1, h2 = s["h0"].clone(), off(s["h0"])
+    a = ssm.ssm_lru_step(s["x"], s["r"], s["i"], s["lam"], h1)
+    b = ssm.ssm_lru_step(off(s["x"]), s["r"], s["i"], s["lam"], h2)
+    assert torch.equal(a, b) and torch.equal(h1, h2)
+
+
+def test_empty():
+    t = inputs(2, 4, 8, BF)
+    z = t["x"][..., :0].contiguous()
+    f = ssm.ssm_lru_fwd(z, z, z, t["lam"], h0=t["h0"], return_state=True)
+    assert f["out"].shape == (2, 4, 0) and torch.equal(f["h_last"], t["h0"])
+    g = ssm.ssm_lru_bwd(z, z, z, z, t["lam"], t["r_bias"], h0=t["h0"], dh_last=t["dh_last"])
+    assert torch.equal(g["dh0"], t["dh_last"]) and not bool(g["dlam"].any()) and not bool(g["dr_bias"].any())
+    e = t["x"][:0].contiguous()
+    g = ssm.ssm_lru_bwd(e, e, e, e, t["lam"])
+    assert g["dx"].shape == (0, 4, 8) and not bool(g["dlam"].any())
+
+
+def test_gradients_against_differences():
+    """Central differences of sum(out w) + sum(h_last v) in fp32; steps of 2^-6 leave a truncation error of
+    order 2^-12 and a rounding error of 2^-24 |loss| 2^6, both far below the tolerance."""
+    t = inputs(1, 2, 12, F32, seed=9)
+    reset = torch.zeros(1, 12, dtype=torch.bool, device="cuda")
+    reset[0, 5] = True
+    names = ("x", "r", "i", "lam", "r_bias", "i_bias", "h0")
+    p = {k: t[k] for k in names}
+
+    def loss(q):
+        f = ssm.ssm_lru_fwd(q["x"], q["r"], q["i"], q["lam"], q["r_bias"], q["i_bias"], h0=q["h0"], reset=reset,
+                            return_state=True)
+        return float((f["out"].double() * t["dout"].double()).sum() + (f["h_last"].double() * t["dh_last"].double()).sum())
+
+    g = ssm.ssm_lru_bwd(t["dout"], p["x"], p["r"], p["i"], p["lam"], p["r_bias"], p["i_bias"], h0=p["h0"], reset=reset,
+                        dh_last=t["dh_last"])
+    for k in names:
+        for at in range(0, p[k].numel(), 3):
+            d = []
+            for s in (2.0 ** -6, -2.0 ** -6):
+                v = p[k].clone()
+                v.view(-1)[at] += s
+                d.append(loss(dict(p, **{k: v})))
+            fd = (d[0] - d[1]) * 2.0 ** 5
+            assert abs(float(g["d" + k].reshape(-1)[at]) - fd) <= 5e-3 + 1e-2 * abs(fd), (k, at)
+
+
+def test_captured_and_on_another_stream():
+    t = inputs(2, 33, 1500, BF)
+    names = ("x", "r", "i", "dout")
+    kw = options(t, FULL)
+
+    def run():
+        f = ssm.ssm_lru_fwd(t["x"], t["r"], t["i"], t["lam"], save_states=True, return_state=True, **kw)
+        g = ssm.ssm_lru_bwd(t["dout"], t["x"], t["r"], t["i"], t["lam"], chunk_states=f["chunk_states"], **kw)
+        return [f["out"], f["h_last"]] + [g[k] for k in sorted(g)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    u = inputs(2, 33, 1500, BF, seed=8)
+    for k in names:
+        t[k].copy_(u[k])
+    eager = [v.clone() for v in run()]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held, eager))
+    with torch.cuda.stream(side):
+        other = run()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, eager))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie beyond 2^31 equal the same rows in a tensor of their own."""
+    Dn, L = 4104, 524288  # 2.15e9 elements
+    x = torch.empty(1, Dn, L, dtype=BF, device="cuda")
+    x.normal_()
+    lam = torch.full((Dn,), -4.0, device="cuda")
+    f = ssm.ssm_lru_fwd(x, x, x, lam, save_states=True)
+    last = x[:, -4:].contiguous()
+    s = ssm.ssm_lru_fwd(last, last, last, lam[-4:].contiguous(), save_states=True)
+    # the few rows run with more warps a row: the same values up to the composition's rounding
+    assert torch.allclose(f["out"][:, -4:].float(), s["out"].float(), rtol=2.0 ** -7, atol=1e-4)
+    del f, s, x
+    torch.cuda.empty_cache()

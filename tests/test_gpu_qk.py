@@ -1,0 +1,241 @@
+"""Normalisation and rotation of queries and keys on the GPU against float64, with derived bounds (layer_refs)."""
+import itertools
+
+import pytest
+import torch
+
+import layer_refs as ref
+import selective_state_space_34_b200 as ssm
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def inputs(Bt, L, Hq, Hk, D, dtype, time=False, seed=0, dout=None):
+    g = torch.Generator().manual_seed(seed)
+    shape = (lambda H: (Bt, H, D, L)) if time else (lambda H: (Bt, L, H, D))
+    n = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    t = {"q": n(*shape(Hq)).to(dtype).cuda(), "k": n(*shape(Hk)).to(dtype).cuda() if Hk else None}
+    dout = dout or dtype
+    t["dq_out"] = n(*shape(Hq)).to(dout).cuda()
+    t["dk_out"] = n(*shape(Hk)).to(dout).cuda() if Hk else None
+    t["q_weight"], t["k_weight"] = (1 + 0.2 * n(D)).cuda(), (1 + 0.2 * n(D)).cuda() if Hk else None
+    t["positions"] = torch.randint(0, 1 << 20, (Bt, L), generator=g).cuda()
+    return t
+
+
+def run_and_check(t, inv_freq, norm=True, interleaved=False, time=False, rot_scale=1.0, eps=1e-6, out_dtype=None,
+                  grads=(F32, BF), weights=True):
+    kw = dict(inv_freq=inv_freq, positions=t["positions"], norm=norm, eps=eps, interleaved=interleaved,
+              rot_scale=rot_scale, layout="bhdl" if time else "blhd")
+    if norm and weights:
+        kw.update(q_weight=t["q_weight"], k_weight=t["k_weight"])
+    q_out, k_out = ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], out_dtype=out_dtype, **kw)
+    for grad in grads:
+        g = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], t["dk_out"], t["k"], grad_dtype=grad, **kw)
+        for side, out in (("q", q_out), ("k", k_out)):
+            if t[side] is None:
+                assert out is None and "dk" not in g
+                continue
+            w = kw.get(side + "_weight")
+            want = ref.qk(t[side], w, inv_freq, t["positions"], norm, eps, interleaved, rot_scale, time,
+                          t["d%s_out" % side])
+            v, b = want["out"]
+            assert out.dtype == (out_dtype or t["q"].dtype) and out.shape == t[side].shape
+            ref.check(side + "_out", out, v, b + ref.HALF[out.dtype] * (v.abs() + b))
+            v, b = want["d"]
+            assert g["d" + side].dtype == grad
+            ref.check("d" + side, g["d" + side], v, b + ref.HALF[grad] * (v.abs() + b))
+            if w is not None:
+                v, b = want["dw"]
+                ref.check("d%s_weight" % side, g["d%s_weight" % side], v, b + ref.EPS * v.abs())
+    return q_out, k_out
+
+
+def freq(rot, dtype=F32, base=10000.0):
+    f, _ = ssm.ssm_rope_inv_freq(rot, base)
+    return f.to(dtype).cuda()
+
+
+# Bt, L, Hq, Hk, D, rot: 16-byte units; groups of lanes that do not fill a warp; head sizes that take the pair path
+STATE_LAST = [(1, 1, 1, 1, 16, 16), (2, 3, 4, 1, 64, 64), (1, 5, 3, 2, 80, 48), (2, 7, 1, 0, 128, 32), (1, 9, 2, 2, 512, 256),
+              (1, 4, 8, 2, 256, 256), (2, 3, 1, 1, 1, 0), (1, 3, 2, 1, 2, 2), (2, 5, 3, 1, 33, 32), (1, 6, 2, 1, 96, 18),
+              (1, 2, 1, 2, 511, 510), (3, 11, 5, 3, 24, 8), (1, 700, 8, 2, 128, 128), (2, 2500, 2, 2, 64, 32)]
+TIME_LAST = [(1, 1, 1, 1, 16, 16), (2, 8, 1, 1, 16, 16), (1, 13, 2, 1, 4, 4), (2, 264, 1, 1, 64, 64), (1, 40, 2, 2, 128, 64),
+             (2, 77, 1, 0, 33, 18), (1, 515, 1, 1, 16, 8), (1, 16, 1, 1, 512, 512), (1, 24, 1, 2, 1, 0), (2, 2304, 1, 1, 16, 16)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("time,case", [(False, c) for c in STATE_LAST] + [(True, c) for c in TIME_LAST])
+def test_forward_and_backward(time, case, interleaved, dtype):
+    Bt, L, Hq, Hk, D, rot = case
+    t = inputs(Bt, L, Hq, Hk, D, dtype, time, seed=D + L)
+    run_and_check(t, freq(rot) if rot else None, True, interleaved, time, rot_scale=1.1)
+
+
+@pytest.mark.parametrize("time", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rotation_alone(dtype, time):
+    for (D, rot), inter in itertools.product(((64, 64), (48, 32), (31, 10)), (False, True)):
+        run_and_check(inputs(2, 24, 3, 1, D, dtype, time), freq(rot), False, inter, time)
+
+
+@pytest.mark.parametrize("time", [False, True])
+def test_types_mixed(time):
+    for dtype, dout, out in ((BF, F32, F32), (BF, F32, BF), (F32, BF, BF), (BF, BF, F32)):
+        run_and_check(inputs(2, 16, 2, 1, 64, dtype, time, dout=dout), freq(32, torch.float64), True, False, time,
+                      out_dtype=out)
+
+
+def test_no_weights_and_odd_types_of_positions():
+    t = inputs(2, 9, 2, 1, 64, F32)
+    run_and_check(t, freq(64), weights=False)
+    kw = dict(inv_freq=freq(64))
+    a = ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], positions=t["positions"], **kw)
+    b = ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], positions=t["positions"].int(), **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    p = torch.arange(77, 77 + 9, device="cuda").expand(2, 9).contiguous()
+    a = ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], positions=p, **kw)
+    b = ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], pos0=77, **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_far_and_negative_positions():
+    t = inputs(1, 6, 1, 1, 32, F32)
+    t["positions"] = torch.tensor([[0, -1, 123456789, 2 ** 31 + 7, 2 ** 40 + 1, -(2 ** 33)]], device="cuda")
+    # the float64 reference's own angle is off by |angle| 2^-53: 2^-12 at 2^40, within 1e-3
+    f = freq(32, torch.float64)
+    q, _ = ssm.ssm_qk_norm_rope_fwd(t["q"], None, inv_freq=f, positions=t["positions"], norm=False)
+    v, b = ref.qk(t["q"], None, f, t["positions"], False, 1e-6, False, 1.0, False)["out"]
+    ref.check("q_out", q, v, b + ref.EPS * v.abs() + torch.tensor([0, 0, 0, 1e-6, 1e-3, 1e-5])[None, :, None, None])
+
+
+def test_strided_views_and_in_place():
+    """Slices of one projection, outputs into slices, and outputs over the inputs."""
+    g = torch.Generator().manual_seed(1)
+    qkv = torch.randn(2, 10, (4 + 2 + 2) * 64, generator=g).to(BF).cuda()
+    heads = qkv.view(2, 10, 8, 64)
+    q, k = heads[:, :, :4], heads[:, :, 4:6]
+    w = (1 + 0.1 * torch.randn(64, generator=g)).cuda()
+    kw = dict(q_weight=w, k_weight=w, inv_freq=freq(64))
+    a = ssm.ssm_qk_norm_rope_fwd(q.contiguous(), k.contiguous(), **kw)
+    b = ssm.ssm_qk_norm_rope_fwd(q, k, **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert b[0].is_contiguous()
+    before = qkv.clone()
+    ssm.ssm_qk_norm_rope_fwd(q, k, out=(q, k), **kw)
+    assert torch.equal(heads[:, :, :4], a[0]) and torch.equal(heads[:, :, 4:6], a[1])
+    assert torch.equal(heads[:, :, 6:], before.view(2, 10, 8, 64)[:, :, 6:])  # what lies between stays
+    # one element off the vector boundary: the pair path, the same values to rounding
+    buf = torch.zeros(a[0].numel() + 1, dtype=BF, device="cuda")
+    odd = buf[1:].view(2, 10, 4, 64)
+    odd.copy_(before.view(2, 10, 8, 64)[:, :, :4])
+    c, _ = ssm.ssm_qk_norm_rope_fwd(odd, None, q_weight=w, inv_freq=kw["inv_freq"])
+    assert torch.allclose(c.float(), a[0].float(), rtol=2.0 ** -7, atol=1e-6)
+    # a repeated (stride 0) input, a transposed batch
+    one = torch.randn(1, 10, 4, 64, generator=g).cuda()
+    r, _ = ssm.ssm_qk_norm_rope_fwd(one.expand(3, 10, 4, 64), None, inv_freq=kw["inv_freq"])
+    s, _ = ssm.ssm_qk_norm_rope_fwd(one, None, inv_freq=kw["inv_freq"])
+    assert all(torch.equal(r[j], s[0]) for j in range(3))
+    lbhd = torch.randn(10, 2, 4, 64, generator=g).cuda()
+    r, _ = ssm.ssm_qk_norm_rope_fwd(lbhd.transpose(0, 1), None, inv_freq=kw["inv_freq"])
+    s, _ = ssm.ssm_qk_norm_rope_fwd(lbhd.transpose(0, 1).contiguous(), None, inv_freq=kw["inv_freq"])
+    assert torch.equal(r, s)
+    time = torch.randn(2, 3, 16, 40, generator=g).cuda()
+    v = time[:, 1:, :, 8:]  # time innermost, a slice of every other axis
+    r, _ = ssm.ssm_qk_norm_rope_fwd(v, None, inv_freq=freq(16), layout="bhdl")
+    s, _ = ssm.ssm_qk_norm_rope_fwd(v.contiguous(), None, inv_freq=freq(16), layout="bhdl")
+    assert torch.equal(r, s)
+    u = v.contiguous()
+    ssm.ssm_qk_norm_rope_fwd(u, None, inv_freq=freq(16), layout="bhdl", out=(u, None))
+    assert torch.equal(u, s)
+
+
+def test_zero_rows_and_nan_rows():
+    t = inputs(1, 6, 2, 1, 64, F32)
+    t["q"][0, 2] = 0.0
+    t["q"][0, 4, 1] = float("nan")
+    q, _ = ssm.ssm_qk_norm_rope_fwd(t["q"], None, inv_freq=freq(64), eps=1e-5)
+    assert bool((q[0, 2] == 0).all()) and bool(q[0, 4, 1].isnan().all())
+    keep = q[0, [0, 1, 3, 5]]
+    assert bool(keep.isfinite().all()) and bool(q[0, 4, 0].isfinite().all())
+
+
+def test_empty_and_missing_sides():
+    f = freq(64)
+    z = torch.empty(2, 0, 4, 64, dtype=BF, device="cuda")
+    w = torch.ones(64, device="cuda")
+    q, k = ssm.ssm_qk_norm_rope_fwd(z, None, q_weight=w, inv_freq=f)
+    assert q.shape == z.shape and k is None
+    g = ssm.ssm_qk_norm_rope_bwd(z, z, q_weight=w, inv_freq=f)
+    assert not bool(g["dq_weight"].any())
+    t = inputs(1, 5, 2, 1, 64, BF)
+    none = t["q"][:, :, :0]
+    q, k = ssm.ssm_qk_norm_rope_fwd(none, t["k"], inv_freq=f)
+    alone, _ = ssm.ssm_qk_norm_rope_fwd(t["k"], None, inv_freq=f)
+    assert q.shape[2] == 0 and torch.equal(k, alone)
+    g = ssm.ssm_qk_norm_rope_bwd(none, none, t["dk_out"], t["k"], q_weight=w, k_weight=w, inv_freq=f)
+    assert not bool(g["dq_weight"].any()) and bool(g["dk_weight"].any())
+
+
+def test_gradients_against_differences():
+    for time in (False, True):
+        t = inputs(1, 4, 1, 1, 6, F32, time, seed=2)
+        f = freq(4)
+        kw = dict(inv_freq=f, positions=t["positions"], layout="bhdl" if time else "blhd", rot_scale=1.2, eps=1e-3)
+
+        def loss(q, w):
+            o, _ = ssm.ssm_qk_norm_rope_fwd(q, None, q_weight=w, **kw)
+            return float((o.double() * t["dq_out"].double()).sum())
+
+        g = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], q_weight=t["q_weight"], **kw)
+        for name, p in (("dq", t["q"]), ("dq_weight", t["q_weight"])):
+            for at in range(p.numel()):
+                d = []
+                for s in (2.0 ** -6, -2.0 ** -6):
+                    v = p.clone()
+                    v.view(-1)[at] += s
+                    d.append(loss(v, t["q_weight"]) if name == "dq" else loss(t["q"], v))
+                fd = (d[0] - d[1]) * 2.0 ** 5
+                assert abs(float(g[name].reshape(-1)[at]) - fd) <= 5e-3 + 1e-2 * abs(fd), (time, name, at)
+
+
+def test_captured_and_two_workspaces():
+    """A graph's scratch is its own: an eager call between capture and replay leaves its results alone."""
+    t = inputs(2, 300, 4, 2, 128, BF)
+    kw = dict(q_weight=t["q_weight"], k_weight=t["k_weight"], inv_freq=freq(128), positions=t["positions"])
+
+    def run(u):
+        g = ssm.ssm_qk_norm_rope_bwd(u["dq_out"], u["q"], u["dk_out"], u["k"], **kw)
+        return list(ssm.ssm_qk_norm_rope_fwd(u["q"], u["k"], **kw)) + [g[k] for k in sorted(g)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(t)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, held = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(run(t))
+    want = [v.clone() for v in run(t)]
+    other = inputs(2, 300, 4, 2, 128, BF, seed=5)
+    graphs[0].replay()
+    with torch.cuda.stream(side):
+        run(other)
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    for h in held:
+        assert all(torch.equal(a, b) for a, b in zip(h, want))
+
+
+def test_backward_needs_no_inputs_without_norm_and_repeats():
+    t = inputs(2, 40, 3, 2, 64, BF)
+    kw = dict(q_weight=t["q_weight"], k_weight=t["k_weight"], inv_freq=freq(64), positions=t["positions"])
+    a = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], t["dk_out"], t["k"], **kw)
+    b = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], t["dk_out"], t["k"], **kw)
+    assert all(torch.equal(a[k], b[k]) for k in a)  # no order of atomics in the sums
+    c = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], torch.full_like(t["q"], float("nan")), norm=False, inv_freq=freq(64))
+    assert bool(c["dq"].isfinite().all())
