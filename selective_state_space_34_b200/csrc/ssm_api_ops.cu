@@ -13,6 +13,7 @@
 namespace {
 
 constexpr int64_t kMaxElems = INT64_C(1) << 50;
+constexpr int64_t kMaxSteps = (INT64_C(1) << 31) - (1 << 13);  // the recurrence counts a row's steps in 32 bits
 
 ssm_status cuda_status(cudaError_t e) { return (ssm_status)ssm::record_cuda_error_code(e); }
 
@@ -30,7 +31,7 @@ ssm_status check_lru(const ssm_lru_args *a, bool need_out, bool *empty) {
   if (!a) return SSM_ERR_NULL;
   if (!dtype_ok(a->in_dtype) || (need_out && !dtype_ok(a->out_dtype))) return SSM_ERR_DTYPE;
   if (a->Bt < 0 || a->Dn <= 0 || a->L < 0) return SSM_ERR_SHAPE;
-  if (!(a->c > 0.f) || !isfinite(a->c)) return SSM_ERR_UNSUPPORTED;
+  if (!(a->c > 0.f) || !isfinite(a->c) || a->L >= kMaxSteps) return SSM_ERR_UNSUPPORTED;
   int64_t rows, elems;
   if (!mul_ok(a->Bt, a->Dn, &rows) || !mul_ok(rows, a->L, &elems) || elems > kMaxElems || rows > kMaxElems)
     return SSM_ERR_SHAPE;

@@ -18,13 +18,14 @@
 //
 // Backward. lambda_t = dout_t + a_{t+1} lambda_{t+1} runs from the end over the same chunks with
 // mu_t = a_t (dout_t + mu_{t+1}), an affine map of what arrives from behind; the states come from the
-// state that entered each chunk (saved by the forward) and a second composition. With
-// rho = la / m^2 the gradient of la times la is q = lambda (la h - rho b): the a^2 / m of
-// d sqrt(1 - a^2) is folded into b / m^2, which stays finite as a -> 1 (rho -> -1/2).
+// state that entered each chunk (saved by the forward) and a second composition. With y = -la and
+// s = 1 - a^2 the gradient of y times y is q = -lambda y (h - b / s): the a^2 / m of d sqrt(1 - a^2) is
+// folded into b / s, and y / s stays finite as a -> 1 (it tends to 1/2).
 //   dx = lambda m g, di~ = lambda b (1 - g), dr~ = q (1 - r), dlam = sum q sigmoid(lam)/softplus(lam)
+// (the kernel carries -q).
 //
-// Precision. The decay goes through em = e^la - 1 (a polynomial for small |la|): 1 - a^2 =
-// -em (2 + em) keeps its relative precision where a is near 1, which a itself in 32 bits does not.
+// Precision. The decay goes through n = 1 - a (a polynomial for small |la|): 1 - a^2 = n + n a keeps its relative
+// precision where a is near 1, which a itself in 32 bits does not.
 #include <type_traits>
 
 #include "ssm_internal.h"
@@ -37,202 +38,359 @@ namespace {
 constexpr int kChunk = 256;  // steps per warp and round: 32 lanes x 8
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxWarps = 16;
-
-// Clamp that keeps NaN (fminf would drop it).
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ float rsqrt_approx(float x) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// min and max that keep NaN (fminf would drop it).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
-// sigmoid(u) and sigmoid(v). Fast: both from one reciprocal, 1/((1+eu)(1+ev)); the exponents are
-// held at 2^60 so that the product stays finite (a gate below 2^-60 reads 2^-60).
-template <bool PRECISE>
-__device__ __forceinline__ void sigmoid2(float u, float v, float &su, float &sv) {
-  if (PRECISE) {
-    su = sigmoid<true>(u);
-    sv = sigmoid<true>(v);
-  } else {
-    const float pu = 1.f + ex2_approx(min_nan(-u * kLog2e, 60.f));
-    const float pv = 1.f + ex2_approx(min_nan(-v * kLog2e, 60.f));
-    const float inv = rcp_approx(pu * pv);
-    su = pv * inv;
-    sv = pu * inv;
+// A lane's 8 elements as 4 pairs (j, j + 4): two half runs of 4 steps in the two halves of the packed fp32
+// instructions, so that the recurrence itself is packed too.
+__device__ __forceinline__ void pairs(const Raw8<__nv_bfloat16> &r, float2 *v) {
+  v[0] = make_float2(__uint_as_float(r.a.x << 16), __uint_as_float(r.a.z << 16));
+  v[1] = make_float2(__uint_as_float(r.a.x & 0xffff0000u), __uint_as_float(r.a.z & 0xffff0000u));
+  v[2] = make_float2(__uint_as_float(r.a.y << 16), __uint_as_float(r.a.w << 16));
+  v[3] = make_float2(__uint_as_float(r.a.y & 0xffff0000u), __uint_as_float(r.a.w & 0xffff0000u));
+}
+__device__ __forceinline__ void pairs(const Raw8<float> &r, float2 *v) {
+  v[0] = make_float2(r.a.x, r.b.x);
+  v[1] = make_float2(r.a.y, r.b.y);
+  v[2] = make_float2(r.a.z, r.b.z);
+  v[3] = make_float2(r.a.w, r.b.w);
+}
+__device__ __forceinline__ void in_order(const float2 *v, float *o) {
+#pragma unroll
+  for (int j = 0; j < 4; j++) o[j] = v[j].x, o[4 + j] = v[j].y;
+}
+
+// What a row's gates need of its parameters. A gate's argument is kept above -42 (its sigmoid above 2^-60), so
+// that the product of two denominators 1 + e^-v stays finite; NaN passes. bf16 inputs are clamped as they are, two
+// at a time (`low`, rounded to bf16, which moves the bound by a 2^-8 part at most).
+struct Gate {
+  float shift;         // -bias log2 e
+  __nv_bfloat162 low;  // -41.5 - bias
+};
+__device__ __forceinline__ Gate gate_of(float bias) {
+  return {-bias * kLog2e, __float2bfloat162_rn(-41.5f - bias)};
+}
+__device__ __forceinline__ void arguments(const Raw8<__nv_bfloat16> &raw, const Gate &g, float2 *t) {
+  Raw8<__nv_bfloat16> c = raw;
+  __nv_bfloat162 *w = reinterpret_cast<__nv_bfloat162 *>(&c.a);
+#pragma unroll
+  for (int j = 0; j < 4; j++) w[j] = __hmax2_nan(w[j], g.low);
+  pairs(c, t);
+#pragma unroll
+  for (int j = 0; j < 4; j++) t[j] = fma2(t[j], splat(-kLog2e), splat(g.shift));
+}
+__device__ __forceinline__ void arguments(const Raw8<float> &raw, const Gate &g, float2 *t) {
+  pairs(raw, t);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    t[j] = fma2(t[j], splat(-kLog2e), splat(g.shift));
+    t[j] = make_float2(min_nan(t[j].x, 60.f), min_nan(t[j].y, 60.f));
   }
 }
+// Both sigmoids from -v log2 e, with one reciprocal: 1/((1+eu)(1+ev)); ev = e^-v on the side, with which
+// 1 - sigmoid(v) = ev sigmoid(v).
+__device__ __forceinline__ void sigmoid2(float2 tu, float2 tv, float2 &su, float2 &sv, float2 &ev) {
+  ev = make_float2(ex2_approx(tv.x), ex2_approx(tv.y));
+  const float2 pu = add2(make_float2(ex2_approx(tu.x), ex2_approx(tu.y)), splat(1.f)), pv = add2(ev, splat(1.f));
+  const float2 d = mul2(pu, pv);
+  const float2 inv = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  su = mul2(pv, inv);
+  sv = mul2(pu, inv);
+}
 
-// a = e^y and em = e^y - 1 for y <= 0, both with relative precision: em by the Taylor polynomial of degree
-// 6 where |y| < 1/4 (the next term is below y^6/5040 < 5e-8 of the sum), a by ex2 beyond (its 2^-22 of 1
-// is 5e-7 of em >= 0.22 at most).
-template <bool PRECISE> __device__ __forceinline__ void decay(float y, float &a, float &em) {
-  if (PRECISE) {
-    em = expm1f(y);
-    a = y > -0.25f ? 1.f + em : expf(y);
-  } else {
-    const float far = ex2_approx(y * kLog2e);
-    float p = fmaf(y, 1.f / 720.f, 1.f / 120.f);
-    p = fmaf(y, p, 1.f / 24.f);
-    p = fmaf(y, p, 1.f / 6.f);
-    p = fmaf(y, p, 0.5f);
-    p = y * fmaf(y, p, 1.f);
-    const bool near = y > -0.25f;
-    em = near ? p : far - 1.f;
-    a = near ? 1.f + p : far;
+// From y = -la >= 0: n = 1 - a and a = e^-y, both with relative precision, s = 1 - a^2 = n + n a, and 1 / sqrt(s).
+// n is y times a polynomial of degree 4 (a minimax fit on [0, 1/2], relative error 8e-8, 2e-7 with the
+// roundings) where y < 1/2, and 1 - ex2 beyond, where a comes from ex2 (2^-22 of it, 3e-7 of n >= 0.39 at most).
+// NEAR: the whole row is in the first case, y <= rate < 1/2. Callers add kTiny to y, so that s is above 0 and
+// the root finite where the decay is 1; m = s / sqrt(s) is then below 2e-18.
+constexpr float kNear = 0.5f, kTiny = 1e-36f;
+template <bool NEAR> __device__ __forceinline__ void decay(float2 y, float2 &a, float2 &s, float2 &is) {
+  float2 p = fma2(y, splat(0x1.bbbf2ap-8f), splat(-0x1.4fe1eap-5f));
+  p = fma2(y, p, splat(0x1.551732p-3f));
+  p = fma2(y, p, splat(-0x1.fffe08p-2f));
+  p = fma2(y, p, splat(0x1.fffffep-1f));
+  float2 n = mul2(y, p);
+  a = fma2(n, splat(-1.f), splat(1.f));
+  if (!NEAR) {
+    const float2 t = mul2(y, splat(-kLog2e));
+    const float2 far = make_float2(ex2_approx(t.x), ex2_approx(t.y)), fn = fma2(far, splat(-1.f), splat(1.f));
+    if (!(y.x < kNear)) a.x = far.x, n.x = fn.x;
+    if (!(y.y < kNear)) a.y = far.y, n.y = fn.y;
   }
+  s = fma2(n, a, n);
+  is = make_float2(rsqrt_approx(s.x), rsqrt_approx(s.y));
 }
 
-// 1 / sqrt(s) of s = 1 - a^2, and 0 where s is 0 (m and b are then 0 too).
-template <bool PRECISE> __device__ __forceinline__ float inv_sqrt(float s) {
-  const float r = PRECISE ? 1.0f / sqrtf(s) : rsqrt_approx(s);
-  return s < 1e-36f ? 0.f : r;
-}
-
-// rate = c softplus(lam) of a row, and its gradient over itself, sigmoid(lam) / softplus(lam) (1 as lam -> -inf).
+// rate = c softplus(lam), the log decay of an open gate.
 __device__ __forceinline__ float decay_rate(float c, float lam) { return c * softplus<true>(lam); }
 
 struct Row {
   int64_t flat;  // flat index of the row's first element
   int f;         // elements of its first group that belong to the row before
-  int64_t len;   // live steps
+  int len;       // live steps (L is below 2^31 - 2^13, so steps and chunks count in 32 bits)
+  int k_lo, k_hi;  // the chunks inside the live steps
+  int n_live;      // chunks that hold live steps
 };
 
 __device__ __forceinline__ Row row_of(const LruParams &p, int64_t row, int64_t b) {
   Row r;
   r.flat = row * p.L;
   r.f = (int)(r.flat & 7);
-  r.len = p.lengths ? imin64(p.L, p.lengths[b] > 0 ? (int64_t)p.lengths[b] : 0) : p.L;
+  r.len = p.lengths ? min((int)p.L, max(p.lengths[b], 0)) : (int)p.L;
+  r.k_lo = r.f ? 1 : 0;
+  r.k_hi = (r.len + r.f) / kChunk;
+  r.n_live = r.len > 0 ? (r.len + r.f + kChunk - 1) / kChunk : 0;
   return r;
 }
 
-// The 8 elements at steps t0 .. t0 + 7 of a row: one vector access where the group lies inside the
-// tensor, element by element otherwise; elements outside [0, len) read as 0 or as a neighbour's.
+// Chunk k of a row lies inside its live steps: no element of a lane is masked.
+__device__ __forceinline__ bool inside(const Row &r, int k) { return k >= r.k_lo && k < r.k_hi; }
+
+// The 8 elements at steps t0 .. t0 + 7 of a row that may reach over its ends: one vector access where the group lies
+// inside the tensor, element by element otherwise; elements outside [0, len) read as 0 or as a neighbour's.
 template <typename T>
-__device__ __forceinline__ void load_group(const T *base, const Row &r, int64_t t0, int64_t total, int vec,
-                                           Raw8<T> &out) {
+__device__ __forceinline__ void load_edge(const T *base, const Row &r, int t0, int64_t total, int vec, Raw8<T> &out) {
   const int64_t at = r.flat + t0;
-  if (t0 + 8 > 0 && t0 < r.len && vec && at >= 0 && at + 8 <= total) {
+  if (vec && t0 < r.len && at >= 0 && at + 8 <= total) {
     ld8(base + at, out);
     return;
   }
   zero8(out);
-  if (t0 + 8 > 0 && t0 < r.len) {
+  if (t0 < r.len) {
 #pragma unroll
     for (int e = 0; e < 8; e++)
       if (t0 + e >= 0 && t0 + e < r.len) put8(out, e, base[at + e]);
   }
 }
 
+// A lane's groups of NT tensors on their way, S rounds of them, in shared memory: each lane copies (cp.async) and
+// reads only its own 16-byte slots, so nothing but its own copies is waited for, and no register holds
+// what is in flight.
+template <typename T, int NT, int S> struct Ring {
+  static constexpr int kHalves = sizeof(T) * 8 / 16;                // 16-byte slots per group
+  static constexpr int kWarpBytes = S * NT * kHalves * 32 * 16;
+  char *base;                                                       // the lane's first slot
+  __device__ __forceinline__ Ring(char *smem, int warp, int lane) : base(smem + warp * kWarpBytes + lane * 16) {}
+  __device__ __forceinline__ char *slot(int stage, int tensor, int half) const {
+    return base + ((stage * NT + tensor) * kHalves + half) * 512;
+  }
+  __device__ __forceinline__ void copy(int stage, int tensor, const T *src) const {
+#pragma unroll
+    for (int h = 0; h < kHalves; h++) cp_async16(slot(stage, tensor, h), reinterpret_cast<const char *>(src) + 16 * h);
+  }
+  __device__ __forceinline__ void put(int stage, int tensor, const Raw8<T> &v) const {
+#pragma unroll
+    for (int h = 0; h < kHalves; h++)
+      *reinterpret_cast<uint4 *>(slot(stage, tensor, h)) = reinterpret_cast<const uint4 *>(&v)[h];
+  }
+  __device__ __forceinline__ void get(int stage, int tensor, Raw8<T> &v) const {
+#pragma unroll
+    for (int h = 0; h < kHalves; h++)
+      reinterpret_cast<uint4 *>(&v)[h] = *reinterpret_cast<const uint4 *>(slot(stage, tensor, h));
+  }
+};
+// Rounds in use and in flight: three of bf16, two of fp32 (twice the bytes each) or of 16 warps. (One-warp rows
+// of bf16: 2 to 5 measured within 5% of each other on every shape.)
+template <typename T, int W> constexpr int kStages = sizeof(T) == 4 || W == 16 ? 2 : 3;
+
 // Store the elements of the group that lie in [0, L).
 template <typename T>
-__device__ __forceinline__ void store_group(T *base, const Row &r, int64_t t0, int64_t L, int vec, const float *v) {
-  if (vec && t0 >= 0 && t0 + 8 <= L) {
-    st8(base + r.flat + t0, v);
+__device__ __forceinline__ void store_group(T *base, const Row &r, bool in, int t0, int L, int vec, const float2 *pv) {
+  float v[8];
+  in_order(pv, v);
+  T *at = base + (r.flat + t0);
+  if (vec && (in || (t0 >= 0 && t0 + 8 <= L))) {
+    st8(at, v);
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; e++)
-    if (t0 + e >= 0 && t0 + e < L) base[r.flat + t0 + e] = from_f32<T>(v[e]);
+    if (t0 + e >= 0 && t0 + e < L) at[e] = from_f32<T>(v[e]);
 }
 
-// Bit e: step t0 + e starts a new sequence.
-__device__ __forceinline__ unsigned load_resets(const uint8_t *reset, int64_t base, int64_t t0, int64_t len) {
-  unsigned m = 0;
+// The reset bytes of steps t0 .. t0 + 7 (0 outside [0, len)): two aligned words and a shift where both lie inside the
+// mask, byte by byte at its ends.
+__device__ __forceinline__ uint64_t load_resets(const LruParams &p, int64_t b, const Row &r, int t0) {
+  if (t0 >= r.len) return 0;
+  const uint8_t *at = p.reset + b * p.L + t0;
+  const int shift = (int)(reinterpret_cast<uintptr_t>(at) & 7);
+  const uint8_t *word = at - shift;
+  if (t0 >= 0 && t0 + 8 <= r.len && word >= p.reset && word + 16 <= p.reset + p.Bt * p.L) {
+    const uint64_t lo = reinterpret_cast<const uint64_t *>(word)[0], hi = reinterpret_cast<const uint64_t *>(word)[1];
+    return shift ? lo >> (8 * shift) | hi << (64 - 8 * shift) : lo;
+  }
+  uint64_t m = 0;
 #pragma unroll
   for (int e = 0; e < 8; e++)
-    if (t0 + e >= 0 && t0 + e < len && reset[base + t0 + e]) m |= 1u << e;
+    if (t0 + e >= 0 && t0 + e < r.len && at[e]) m |= UINT64_C(1) << (8 * e);
   return m;
 }
 
 // x -> P x + H after x -> Q x + G, where a P of 0 cuts off whatever came before (a reset: NaN and
 // infinity of an earlier sequence must not reach this one through 0 * NaN).
-template <bool RESET> __device__ __forceinline__ float after(float P, float x, float H) {
-  return RESET && P == 0.f ? H : fmaf(P, x, H);
+template <bool CUT> __device__ __forceinline__ float after(float P, float x, float H) {
+  return CUT && P == 0.f ? H : fmaf(P, x, H);
+}
+template <bool CUT> __device__ __forceinline__ float2 after2(float2 P, float2 x, float2 H) {
+  if (CUT) return make_float2(after<true>(P.x, x.x, H.x), after<true>(P.y, x.y, H.y));
+  return fma2(P, x, H);
 }
 // The factor of the same composition, with the same cut.
-template <bool RESET> __device__ __forceinline__ float times(float P, float Q) {
-  return RESET && P == 0.f ? 0.f : P * Q;
+template <bool CUT> __device__ __forceinline__ float times(float P, float Q) {
+  return CUT && P == 0.f ? 0.f : P * Q;
 }
+template <bool CUT> __device__ __forceinline__ float2 times2(float2 P, float2 Q) {
+  if (CUT) return make_float2(times<true>(P.x, Q.x), times<true>(P.y, Q.y));
+  return mul2(P, Q);
+}
+
+// The maps of a lane's two half runs, and of the lanes up to and including this one.
+template <bool CUT>
+__device__ __forceinline__ void compose(const float2 *a, const float2 *b, float2 &P2, float2 &H2) {
+  P2 = a[0];
+  H2 = b[0];
+#pragma unroll
+  for (int j = 1; j < 4; j++) {
+    H2 = after2<CUT>(a[j], H2, b[j]);
+    P2 = times2<CUT>(a[j], P2);
+  }
+}
+template <bool CUT> __device__ __forceinline__ void scan_up(int lane, float &P, float &H) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float Q = __shfl_up_sync(kFull, P, off), G = __shfl_up_sync(kFull, H, off);
+    if (lane >= off) {
+      H = after<CUT>(P, G, H);
+      P = times<CUT>(P, Q);
+    }
+  }
+}
+template <bool CUT> __device__ __forceinline__ void scan_down(int lane, float &S, float &M) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float Z = __shfl_down_sync(kFull, S, off), N = __shfl_down_sync(kFull, M, off);
+    if (lane + off < 32) {
+      M = after<CUT>(S, N, M);
+      S = times<CUT>(S, Z);
+    }
+  }
+}
+
+// Element e of a pair array.
+__device__ __forceinline__ float &elem(float2 *v, int e) { return e < 4 ? v[e].x : v[e - 4].y; }
 
 }  // namespace
 
 // ---- forward -----------------------------------------------------------------------------------
 
-// W warps per row; with W = 1 the CTA's four warps take four rows.
+// A CTA of W warps per row. One-warp CTAs for the common case: as many rows as an SM has warps, no barriers, and a
+// tail of single rows (4 x 4096 x 4096 bf16 forward + backward 267 us, with four rows per CTA 283 us).
 template <typename T, typename Tout, int W, bool RESET>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) lru_fwd_kernel(const LruParams p) {
-  constexpr bool PRECISE = sizeof(T) == 4;
+__global__ void __launch_bounds__(32 * W, W <= 4 ? 28 / W : 1) lru_fwd_kernel(const __grid_constant__ LruParams p) {
+  extern __shared__ __align__(16) char ring_smem[];
+  constexpr int S = kStages<T, W>;
   __shared__ float sP[2][W], sH[2][W];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
-  if (row >= p.Bt * p.Dn) return;  // whole warps, and with W > 1 never (one CTA per row)
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;
   const int64_t b = row / p.Dn, d = row - b * p.Dn;
   const Row R = row_of(p, row, b);
   const int64_t total = p.Bt * p.Dn * p.L;
   const T *x = static_cast<const T *>(p.x), *rg = static_cast<const T *>(p.r), *ig = static_cast<const T *>(p.i);
-  const float rb = p.r_bias ? p.r_bias[d] : 0.f, ib = p.i_bias ? p.i_bias[d] : 0.f;
+  const int L = (int)p.L, n_ck = (L + R.f + kChunk - 1) / kChunk;
+  const Ring<T, 3, S> ring(ring_smem, w, lane);
+  uint64_t ncut = 0;
+  auto fetch = [&](int k, int stage) {
+    const int t0 = k * kChunk + 8 * lane - R.f;
+    if (p.vec && inside(R, k)) {
+      const int64_t at = R.flat + t0;
+      ring.copy(stage, 0, x + at);
+      ring.copy(stage, 1, rg + at);
+      ring.copy(stage, 2, ig + at);
+    } else {
+      Raw8<T> v;
+      load_edge(x, R, t0, total, p.vec, v);
+      ring.put(stage, 0, v);
+      load_edge(rg, R, t0, total, p.vec, v);
+      ring.put(stage, 1, v);
+      load_edge(ig, R, t0, total, p.vec, v);
+      ring.put(stage, 2, v);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int j = 0; j < S - 1; j++) fetch(w + j * W, j);
+  if (RESET) ncut = load_resets(p, b, R, w * kChunk + 8 * lane - R.f);
+  const Gate gr = gate_of(p.r_bias ? p.r_bias[d] : 0.f), gi = gate_of(p.i_bias ? p.i_bias[d] : 0.f);
   const float rate = decay_rate(p.c, p.lam[d]);
   float carry = p.h0 ? p.h0[row] : 0.f;  // the state that enters the round
-  const int64_t n_ck = (p.L + R.f + kChunk - 1) / kChunk;
-  const int w = W == 1 ? 0 : warp;
-  Raw8<T> nx, nr, ni;
-  {
-    const int64_t t0 = (int64_t)w * kChunk + 8 * lane - R.f;
-    load_group(x, R, t0, total, p.vec, nx);
-    load_group(rg, R, t0, total, p.vec, nr);
-    load_group(ig, R, t0, total, p.vec, ni);
-  }
-  int buf = 0;
-  for (int64_t k0 = 0; k0 < n_ck; k0 += W, buf ^= 1) {
-    const int64_t k = k0 + w;
-    const int64_t t0 = k * kChunk + 8 * lane - R.f;
-    float xv[8], a[8], bb[8], tmp[8];
-    unpack8(nx, xv);
-    unpack8(nr, a);
-    unpack8(ni, tmp);
-    {  // the next round's inputs
-      const int64_t tn = t0 + (int64_t)W * kChunk;
-      load_group(x, R, tn, total, p.vec, nx);
-      load_group(rg, R, tn, total, p.vec, nr);
-      load_group(ig, R, tn, total, p.vec, ni);
+  int buf = 0, stage = 0;
+  const int rounds = (R.n_live + W - 1) / W;
+  for (int it = 0; it < rounds; it++, buf ^= 1) {
+    const int k = it * W + w;
+    const bool in = inside(R, k);
+    const int t0 = k * kChunk + 8 * lane - R.f;
+    float2 a[4], bb[4], r[4], g[4];
+    fetch(k + (S - 1) * W, stage == 0 ? S - 1 : stage - 1);  // into the slots of the round before
+    cp_async_wait<S - 1>();
+    {
+      Raw8<T> v;
+      ring.get(stage, 1, v);
+      arguments(v, gr, r);
+      ring.get(stage, 2, v);
+      arguments(v, gi, g);
+      ring.get(stage, 0, v);
+      pairs(v, bb);
     }
-    const unsigned cut = RESET ? load_resets(p.reset, b * p.L, t0, R.len) : 0u;
-    const bool whole = t0 >= 0 && t0 + 8 <= R.len;
+    stage = stage == S - 1 ? 0 : stage + 1;
+    const uint64_t cut = ncut;
+    if (RESET) ncut = load_resets(p, b, R, t0 + W * kChunk);
+    auto coefficients = [&](auto near) {
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      float r, g;
-      sigmoid2<PRECISE>(a[e] + rb, tmp[e] + ib, r, g);
-      float em;
-      decay<PRECISE>(-rate * r, a[e], em);
-      const float s = -em * (em + 2.f);
-      const float m = s * inv_sqrt<PRECISE>(s);
-      if (RESET && (cut >> e & 1)) a[e] = 0.f;
-      bb[e] = m * g * xv[e];
-    }
-    if (!whole) {
+      for (int j = 0; j < 4; j++) {
+        float2 ev, sq, is;
+        sigmoid2(r[j], g[j], r[j], g[j], ev);
+        decay<decltype(near)::value>(fma2(r[j], splat(rate), splat(kTiny)), a[j], sq, is);
+        bb[j] = mul2(mul2(mul2(sq, is), g[j]), bb[j]);
+      }
+    };
+    if (rate < kNear) coefficients(std::true_type());
+    else coefficients(std::false_type());
+    if (!in) {
 #pragma unroll
       for (int e = 0; e < 8; e++)
-        if (t0 + e < 0 || t0 + e >= R.len) a[e] = 1.f, bb[e] = 0.f;
+        if (t0 + e < 0 || t0 + e >= R.len) elem(a, e) = 1.f, elem(bb, e) = 0.f;
     }
-    float P = a[0], H = bb[0];
+    float2 P2, H2;
+    float P, H;
+    const bool cuts = RESET && __any_sync(kFull, cut != 0);
+    if (cuts) {
 #pragma unroll
-    for (int e = 1; e < 8; e++) {
-      H = after<RESET>(a[e], H, bb[e]);
-      P = times<RESET>(a[e], P);
+      for (int e = 0; e < 8; e++)
+        if (cut >> (8 * e) & 0xff) elem(a, e) = 0.f;
+      compose<true>(a, bb, P2, H2);
+      P = times<true>(P2.y, P2.x);
+      H = after<true>(P2.y, H2.x, H2.y);
+      scan_up<true>(lane, P, H);
+    } else {
+      compose<false>(a, bb, P2, H2);
+      P = P2.y * P2.x;
+      H = fmaf(P2.y, H2.x, H2.y);
+      scan_up<false>(lane, P, H);
     }
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const float Q = __shfl_up_sync(kFull, P, off), G = __shfl_up_sync(kFull, H, off);
-      if (lane >= off) {
-        H = after<RESET>(P, G, H);
-        P = times<RESET>(P, Q);
-      }
-    }
-    float in = carry;  // the state that enters this warp's chunk
+    float into = carry;  // the state that enters this warp's chunk
     if (W > 1) {
       if (lane == 31) {
         sP[buf][w] = P;
@@ -242,132 +400,173 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) lru_fwd_kernel(const Lr
       float c = carry;
 #pragma unroll
       for (int v = 0; v < W; v++) {
-        if (v == w) in = c;
+        if (v == w) into = c;
         c = after<RESET>(sP[buf][v], c, sH[buf][v]);
       }
       carry = c;
     }
-    // the state that enters the lane
+    // the states of the two half runs, from the state that enters each
     const float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
-    float h = lane == 0 ? in : after<RESET>(Pe, in, He);
-    if (W == 1) carry = after<RESET>(__shfl_sync(kFull, P, 31), carry, __shfl_sync(kFull, H, 31));
-    if (k < n_ck) {
-      if (p.states && lane == 0) p.states[row * p.n_states + k] = in;
-      if (p.out) {
+    float2 h;
+    h.x = lane == 0 ? into : after<RESET>(Pe, into, He);
+    h.y = after<RESET>(P2.x, h.x, H2.x);
+    if (p.states && lane == 0 && k < n_ck) p.states[row * p.n_states + k] = into;
+    if (cuts) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) bb[e] = h = after<RESET>(a[e], h, bb[e]);
-        if (!whole) {
+      for (int j = 0; j < 4; j++) bb[j] = h = after2<true>(a[j], h, bb[j]);
+    } else {
 #pragma unroll
-          for (int e = 0; e < 8; e++)
-            if (t0 + e >= R.len) bb[e] = 0.f;
-        }
-        store_group(static_cast<Tout *>(p.out), R, t0, p.L, p.vec_out, bb);
+      for (int j = 0; j < 4; j++) bb[j] = h = fma2(a[j], h, bb[j]);
+    }
+    if (W == 1) carry = __shfl_sync(kFull, h.y, 31);
+    if (p.out && k < n_ck) {
+      if (!in) {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+          if (t0 + e >= R.len) elem(bb, e) = 0.f;
       }
+      store_group(static_cast<Tout *>(p.out), R, in, t0, L, p.vec_out, bb);
     }
   }
-  if (p.h_last && threadIdx.x % (32 * W) == 0) p.h_last[row] = carry;
+  for (int k = rounds * W + w; k < n_ck; k += W) {  // behind the last live step
+    const float2 none[4] = {};
+    if (p.states && lane == 0) p.states[row * p.n_states + k] = carry;
+    if (p.out) store_group(static_cast<Tout *>(p.out), R, false, k * kChunk + 8 * lane - R.f, L, p.vec_out, none);
+  }
+  if (p.h_last && threadIdx.x == 0) p.h_last[row] = carry;
 }
 
 // ---- backward ----------------------------------------------------------------------------------
 
 template <typename T, typename Tg, int W, bool RESET>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) lru_bwd_kernel(const LruBwdParams q) {
-  constexpr bool PRECISE = sizeof(T) == 4;
+__global__ void __launch_bounds__(32 * W, W <= 4 ? 16 / W : 1) lru_bwd_kernel(const __grid_constant__ LruBwdParams q) {
   const LruParams &p = q.f;
+  extern __shared__ __align__(16) char ring_smem[];
+  constexpr int S = kStages<T, W>;
   __shared__ float sP[2][W], sM[2][W];
   __shared__ float sS[3][W];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
-  if (row >= p.Bt * p.Dn) return;  // whole warps, and with W > 1 never
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;
   const int64_t b = row / p.Dn, d = row - b * p.Dn;
   const Row R = row_of(p, row, b);
   const int64_t total = p.Bt * p.Dn * p.L;
   const T *x = static_cast<const T *>(p.x), *rg = static_cast<const T *>(p.r), *ig = static_cast<const T *>(p.i);
   const T *dout = static_cast<const T *>(q.dout);
-  const float rb = p.r_bias ? p.r_bias[d] : 0.f, ib = p.i_bias ? p.i_bias[d] : 0.f;
-  const float lam = p.lam[d];
-  const float rate = decay_rate(p.c, lam);
-  float carry = q.dh_last ? q.dh_last[row] : 0.f;  // mu arriving at the round's last step from behind
-  const int64_t n_ck = (p.L + R.f + kChunk - 1) / kChunk;
-  const int64_t rounds = (n_ck + W - 1) / W;
-  const int w = W == 1 ? 0 : warp;
-  float sum_q = 0.f, sum_r = 0.f, sum_i = 0.f;
-  Raw8<T> nx, nr, ni, nd;
+  const int L = (int)p.L, n_ck = (L + R.f + kChunk - 1) / kChunk, rounds = (R.n_live + W - 1) / W;
+  float2 sum_q = splat(0.f), sum_r = splat(0.f), sum_i = splat(0.f);
+  const Ring<T, 4, S> ring(ring_smem, w, lane);
+  auto fetch = [&](int k, int stage) {
+    const int t0 = k * kChunk + 8 * lane - R.f;
+    if (k < 0) {
+    } else if (p.vec && inside(R, k)) {
+      const int64_t at = R.flat + t0;
+      ring.copy(stage, 0, x + at);
+      ring.copy(stage, 1, rg + at);
+      ring.copy(stage, 2, ig + at);
+      ring.copy(stage, 3, dout + at);
+    } else {
+      Raw8<T> v;
+      load_edge(x, R, t0, total, p.vec, v);
+      ring.put(stage, 0, v);
+      load_edge(rg, R, t0, total, p.vec, v);
+      ring.put(stage, 1, v);
+      load_edge(ig, R, t0, total, p.vec, v);
+      ring.put(stage, 2, v);
+      load_edge(dout, R, t0, total, p.vec, v);
+      ring.put(stage, 3, v);
+    }
+    cp_async_commit();
+  };
+  uint64_t ncut = 0;
   float nh = 0.f;
-  {
-    const int64_t k = (rounds - 1) * W + w;
-    const int64_t t0 = k * kChunk + 8 * lane - R.f;
-    load_group(x, R, t0, total, p.vec, nx);
-    load_group(rg, R, t0, total, p.vec, nr);
-    load_group(ig, R, t0, total, p.vec, ni);
-    load_group(dout, R, t0, total, p.vec, nd);
-    if (k < n_ck) nh = p.states[row * p.n_states + k];
-  }
-  int buf = 0;
-  for (int64_t it = rounds - 1; it >= 0; it--, buf ^= 1) {
-    const int64_t k = it * W + w;
-    const int64_t t0 = k * kChunk + 8 * lane - R.f;
-    float a[8], la[8], u[8], v[8], z[8], bb[8], dv[8];
-    unpack8(nx, bb);
-    unpack8(nr, a);
-    unpack8(ni, v);
-    unpack8(nd, dv);
-    const float hin = nh;
-    if (it > 0) {  // the next round's inputs
-      const int64_t tn = t0 - (int64_t)W * kChunk;
-      load_group(x, R, tn, total, p.vec, nx);
-      load_group(rg, R, tn, total, p.vec, nr);
-      load_group(ig, R, tn, total, p.vec, ni);
-      load_group(dout, R, tn, total, p.vec, nd);
-      nh = p.states[row * p.n_states + k - W];
-    }
-    const unsigned cut = RESET ? load_resets(p.reset, b * p.L, t0, R.len) : 0u;
-    const bool whole = t0 >= 0 && t0 + 8 <= R.len;
+  auto fetch_small = [&](int k) {
+    if (RESET) ncut = load_resets(p, b, R, k * kChunk + 8 * lane - R.f);
+    if (k >= 0 && k < n_ck) nh = p.states[row * p.n_states + k];
+  };
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      float r, g;
-      sigmoid2<PRECISE>(a[e] + rb, v[e] + ib, r, g);
-      la[e] = -rate * r;
-      float em;
-      decay<PRECISE>(la[e], a[e], em);
-      const float s = -em * (em + 2.f);
-      const float is = inv_sqrt<PRECISE>(s);
-      if (RESET && (cut >> e & 1)) a[e] = 0.f;
-      u[e] = s * is * g;             // m g
-      bb[e] *= u[e];                 // m g x
-      v[e] = bb[e] * (1.f - g);
-      z[e] = la[e] * is * is * bb[e];  // rho b
+  for (int j = 0; j < S - 1; j++) fetch((rounds - 1 - j) * W + w, j);
+  fetch_small((rounds - 1) * W + w);
+  const Gate gr = gate_of(p.r_bias ? p.r_bias[d] : 0.f), gi = gate_of(p.i_bias ? p.i_bias[d] : 0.f);
+  const float lam = p.lam[d];
+  const float rate = decay_rate(p.c, lam), inv_rate = rate > 0.f ? 1.f / rate : 0.f;
+  float carry = q.dh_last ? q.dh_last[row] : 0.f;  // mu arriving at the round's last step from behind
+  int buf = 0, stage = 0;
+  for (int it = rounds - 1; it >= 0; it--, buf ^= 1) {
+    const int k = it * W + w;
+    const bool in = inside(R, k);
+    const int t0 = k * kChunk + 8 * lane - R.f;
+    float2 a[4], y[4], u[4], v[4], z[4], bb[4], dv[4];
+    fetch(k - (S - 1) * W, stage == 0 ? S - 1 : stage - 1);  // into the slots of the round before
+    cp_async_wait<S - 1>();
+    {
+      Raw8<T> raw;
+      ring.get(stage, 1, raw);
+      arguments(raw, gr, y);
+      ring.get(stage, 2, raw);
+      arguments(raw, gi, v);
+      ring.get(stage, 0, raw);
+      pairs(raw, bb);
+      ring.get(stage, 3, raw);
+      pairs(raw, dv);
     }
-    if (!whole) {
+    stage = stage == S - 1 ? 0 : stage + 1;
+    const float hin = nh;
+    const uint64_t cut = ncut;
+    if (it > 0) fetch_small(k - W);
+    auto coefficients = [&](auto near) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        float2 r, g, ev, sq, is;
+        sigmoid2(y[j], v[j], r, g, ev);
+        y[j] = fma2(r, splat(rate), splat(kTiny));
+        decay<decltype(near)::value>(y[j], a[j], sq, is);
+        u[j] = mul2(mul2(sq, is), g);                     // m g
+        bb[j] = mul2(bb[j], u[j]);                        // m g x
+        v[j] = mul2(bb[j], mul2(ev, g));                  // b (1 - g)
+        z[j] = mul2(mul2(mul2(y[j], is), is), bb[j]);     // y b / s
+      }
+    };
+    if (rate < kNear) coefficients(std::true_type());
+    else coefficients(std::false_type());
+    if (!in) {
 #pragma unroll
       for (int e = 0; e < 8; e++)
-        if (t0 + e < 0 || t0 + e >= R.len) a[e] = 1.f, bb[e] = la[e] = u[e] = v[e] = z[e] = dv[e] = 0.f;
+        if (t0 + e < 0 || t0 + e >= R.len) {
+          elem(a, e) = 1.f;
+          elem(bb, e) = elem(y, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+        }
     }
-    // the states, from the state that entered the chunk
-    float P = a[0], H = bb[0];
+    // the states' maps forwards, and mu -> S mu + M of what leaves the lane's first step backwards
+    float2 P2, H2, M2 = splat(0.f);
+    float P, H, S, M;
+    const bool cuts = RESET && __any_sync(kFull, cut != 0);
+    if (cuts) {
 #pragma unroll
-    for (int e = 1; e < 8; e++) {
-      H = after<RESET>(a[e], H, bb[e]);
-      P = times<RESET>(a[e], P);
+      for (int e = 0; e < 8; e++)
+        if (cut >> (8 * e) & 0xff) elem(a, e) = 0.f;
+      compose<true>(a, bb, P2, H2);
+      // a cut stops mu whatever the other factors are (NaN, in a sequence of its own)
+      const float Sx = cut & 0xffffffffu ? 0.f : P2.x, Sy = cut >> 32 ? 0.f : P2.y;
+#pragma unroll
+      for (int j = 3; j >= 0; j--) M2 = after2<true>(a[j], add2(dv[j], M2), splat(0.f));
+      P = times<true>(P2.y, P2.x);
+      H = after<true>(P2.y, H2.x, H2.y);
+      S = times<true>(Sx, Sy);
+      M = after<true>(Sx, M2.y, M2.x);
+      P2 = make_float2(P2.x, Sy);
+      scan_up<true>(lane, P, H);
+      scan_down<true>(lane, S, M);
+    } else {
+      compose<false>(a, bb, P2, H2);
+#pragma unroll
+      for (int j = 3; j >= 0; j--) M2 = mul2(a[j], add2(dv[j], M2));
+      P = S = P2.y * P2.x;
+      H = fmaf(P2.y, H2.x, H2.y);
+      M = fmaf(P2.x, M2.y, M2.x);
+      scan_up<false>(lane, P, H);
+      scan_down<false>(lane, S, M);
     }
-    // and what leaves the lane's first step backwards: mu -> P mu + M
-    float S = RESET && cut ? 0.f : P, M = 0.f;
-#pragma unroll
-    for (int e = 7; e >= 0; e--) M = after<RESET>(a[e], dv[e] + M, 0.f);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const float Q = __shfl_up_sync(kFull, P, off), G = __shfl_up_sync(kFull, H, off);
-      const float Z = __shfl_down_sync(kFull, S, off), N = __shfl_down_sync(kFull, M, off);
-      if (lane >= off) {
-        H = after<RESET>(P, G, H);
-        P = times<RESET>(P, Q);
-      }
-      if (lane + off < 32) {
-        M = after<RESET>(S, N, M);
-        S = times<RESET>(S, Z);
-      }
-    }
-    float in = carry;  // mu arriving behind this warp's chunk
+    float into = carry;  // mu arriving behind this warp's chunk
     if (W > 1) {
       if (lane == 0) {
         sP[buf][w] = S;
@@ -377,70 +576,83 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) lru_bwd_kernel(const Lr
       float c = carry;
 #pragma unroll
       for (int o = W - 1; o >= 0; o--) {
-        if (o == w) in = c;
+        if (o == w) into = c;
         c = after<RESET>(sP[buf][o], c, sM[buf][o]);
       }
       carry = c;
     }
     const float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
-    float h = lane == 0 ? hin : after<RESET>(Pe, hin, He);
     const float Se = __shfl_down_sync(kFull, S, 1), Me = __shfl_down_sync(kFull, M, 1);
-    float mu = lane == 31 ? in : after<RESET>(Se, in, Me);
-    if (W == 1) carry = after<RESET>(__shfl_sync(kFull, S, 0), carry, __shfl_sync(kFull, M, 0));
+    float2 h, mu;
+    h.x = lane == 0 ? hin : after<RESET>(Pe, hin, He);
+    h.y = after<RESET>(P2.x, h.x, H2.x);
+    mu.y = lane == 31 ? into : after<RESET>(Se, into, Me);
+    mu.x = after<RESET>(P2.y, mu.y, M2.y);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      h = RESET && cuts ? after2<true>(a[j], h, bb[j]) : fma2(a[j], h, bb[j]);
+      z[j] = fma2(z[j], splat(-1.f), mul2(y[j], h));  // y (h - b / s)
+    }
+#pragma unroll
+    for (int j = 3; j >= 0; j--) {
+      const float2 lm = add2(dv[j], mu);
+      mu = RESET && cuts ? after2<true>(a[j], lm, splat(0.f)) : mul2(a[j], lm);
+      u[j] = mul2(u[j], lm);
+      v[j] = mul2(v[j], lm);
+      bb[j] = mul2(z[j], lm);
+      z[j] = mul2(bb[j], fma2(y[j], splat(inv_rate), splat(-1.f)));  // -(1 - r) = y / rate - 1
+    }
+    if (W == 1) carry = __shfl_sync(kFull, mu.x, 0);
     if (k >= n_ck) continue;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      h = after<RESET>(a[e], h, bb[e]);
-      z[e] = fmaf(la[e], h, -z[e]);  // la h - rho b
-    }
-    const float inv_rate = rate > 0.f ? 1.f / rate : 0.f;
-#pragma unroll
-    for (int e = 7; e >= 0; e--) {
-      const float lm = dv[e] + mu;
-      mu = after<RESET>(a[e], lm, 0.f);
-      u[e] *= lm;
-      v[e] *= lm;
-      const float g = lm * z[e];
-      z[e] = g * fmaf(la[e], inv_rate, 1.f);  // 1 - r = 1 + la / rate
-      bb[e] = g;
-    }
-    if (!whole) {  // steps outside the row hold 0 (0 times an infinite lambda would not be)
+    if (!in) {  // steps outside the row hold 0 (0 times an infinite lambda would not be)
 #pragma unroll
       for (int e = 0; e < 8; e++)
-        if (t0 + e < 0 || t0 + e >= R.len) u[e] = v[e] = z[e] = bb[e] = 0.f;
+        if (t0 + e < 0 || t0 + e >= R.len) elem(u, e) = elem(v, e) = elem(z, e) = elem(bb, e) = 0.f;
     }
-    if (q.dx) store_group(static_cast<Tg *>(q.dx), R, t0, p.L, q.vec_grad, u);
-    if (q.di) store_group(static_cast<Tg *>(q.di), R, t0, p.L, q.vec_grad, v);
-    if (q.dr) store_group(static_cast<Tg *>(q.dr), R, t0, p.L, q.vec_grad, z);
+    if (q.dx) store_group(static_cast<Tg *>(q.dx), R, in, t0, L, q.vec_grad, u);
+    if (q.di) store_group(static_cast<Tg *>(q.di), R, in, t0, L, q.vec_grad, v);
+    if (q.dr) store_group(static_cast<Tg *>(q.dr), R, in, t0, L, q.vec_grad, z);
 #pragma unroll
-    for (int e = 0; e < 8; e++) sum_q += bb[e], sum_r += z[e], sum_i += v[e];
+    for (int j = 0; j < 4; j++) {
+      sum_q = add2(sum_q, bb[j]);
+      sum_r = add2(sum_r, z[j]);
+      sum_i = add2(sum_i, v[j]);
+    }
   }
-  if (q.dh0 && threadIdx.x % (32 * W) == 0) q.dh0[row] = carry;
+  for (int k = rounds * W + w; k < n_ck; k += W) {  // behind the last live step
+    const float2 none[4] = {};
+    const int t0 = k * kChunk + 8 * lane - R.f;
+    if (q.dx) store_group(static_cast<Tg *>(q.dx), R, false, t0, L, q.vec_grad, none);
+    if (q.di) store_group(static_cast<Tg *>(q.di), R, false, t0, L, q.vec_grad, none);
+    if (q.dr) store_group(static_cast<Tg *>(q.dr), R, false, t0, L, q.vec_grad, none);
+  }
+  if (q.dh0 && threadIdx.x == 0) q.dh0[row] = carry;
   if (!q.p_dlam && !q.p_dr && !q.p_di) return;
+  float sq = sum_q.x + sum_q.y, sr = sum_r.x + sum_r.y, si = sum_i.x + sum_i.y;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) {
-    sum_q += __shfl_xor_sync(kFull, sum_q, off);
-    sum_r += __shfl_xor_sync(kFull, sum_r, off);
-    sum_i += __shfl_xor_sync(kFull, sum_i, off);
+    sq += __shfl_xor_sync(kFull, sq, off);
+    sr += __shfl_xor_sync(kFull, sr, off);
+    si += __shfl_xor_sync(kFull, si, off);
   }
   if (W > 1) {
-    if (lane == 0) sS[0][w] = sum_q, sS[1][w] = sum_r, sS[2][w] = sum_i;
+    if (lane == 0) sS[0][w] = sq, sS[1][w] = sr, sS[2][w] = si;
     __syncthreads();
     if (threadIdx.x != 0) return;
-    sum_q = sum_r = sum_i = 0.f;
-    for (int o = 0; o < W; o++) sum_q += sS[0][o], sum_r += sS[1][o], sum_i += sS[2][o];
+    sq = sr = si = 0.f;
+    for (int o = 0; o < W; o++) sq += sS[0][o], sr += sS[1][o], si += sS[2][o];
   } else if (lane != 0) {
     return;
   }
   // sigmoid / softplus: 1 as lam -> -inf, where softplus reaches 0
   const float sp = softplus<true>(lam);
-  if (q.p_dlam) q.p_dlam[row] = sum_q * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
-  if (q.p_dr) q.p_dr[row] = sum_r;
-  if (q.p_di) q.p_di[row] = sum_i;
+  if (q.p_dlam) q.p_dlam[row] = -sq * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
+  if (q.p_dr) q.p_dr[row] = sr;
+  if (q.p_di) q.p_di[row] = si;
 }
 
 // Per-row sums over the batch in a fixed order.
-__global__ void __launch_bounds__(128) lru_param_sum_kernel(const LruBwdParams q) {
+__global__ void __launch_bounds__(128) lru_param_sum_kernel(const __grid_constant__ LruBwdParams q) {
   const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (d >= q.f.Dn) return;
   const float *src[3] = {q.p_dlam, q.p_dr, q.p_di};
@@ -458,8 +670,7 @@ __global__ void __launch_bounds__(128) lru_param_sum_kernel(const LruBwdParams q
 
 // V consecutive channels a thread (V = 4: Dn a multiple of 4 and every pointer on a vector boundary).
 template <typename T, typename Tout, int V>
-__global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
-  constexpr bool PRECISE = sizeof(T) == 4;
+__global__ void __launch_bounds__(128) lru_step_kernel(const __grid_constant__ LruStepParams p) {
   const int64_t i0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
   if (i0 >= p.Bt * p.Dn) return;
   const int64_t d = i0 % p.Dn;
@@ -467,7 +678,7 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
   alignas(16) float h[V], lam[V], rb[V], ib[V];
   alignas(16) Tout o[V];
   if constexpr (V == 4) {
-    using V4 = typename std::conditional<PRECISE, float4, uint2>::type;
+    using V4 = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
     *reinterpret_cast<V4 *>(x) = *reinterpret_cast<const V4 *>(static_cast<const T *>(p.x) + i0);
     *reinterpret_cast<V4 *>(r) = *reinterpret_cast<const V4 *>(static_cast<const T *>(p.r) + i0);
     *reinterpret_cast<V4 *>(g) = *reinterpret_cast<const V4 *>(static_cast<const T *>(p.i) + i0);
@@ -486,14 +697,19 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const LruStepParams p) {
     ib[0] = p.i_bias ? p.i_bias[d] : 0.f;
   }
 #pragma unroll
-  for (int e = 0; e < V; e++) {
-    float rr, gg;
-    sigmoid2<PRECISE>(to_f32(r[e]) + rb[e], to_f32(g[e]) + ib[e], rr, gg);
-    float a, em;
-    decay<PRECISE>(-decay_rate(p.c, lam[e]) * rr, a, em);
-    const float s = -em * (em + 2.f);
-    h[e] = fmaf(a, h[e], s * inv_sqrt<PRECISE>(s) * gg * to_f32(x[e]));
-    o[e] = from_f32<Tout>(h[e]);
+  for (int e = 0; e < V; e += 2) {  // two channels a packed instruction (V = 1: the same one twice)
+    const int f = V == 1 ? e : e + 1;
+    float2 t = fma2(make_float2(to_f32(r[e]), to_f32(r[f])), splat(-kLog2e), mul2(make_float2(rb[e], rb[f]), splat(-kLog2e)));
+    float2 n = fma2(make_float2(to_f32(g[e]), to_f32(g[f])), splat(-kLog2e), mul2(make_float2(ib[e], ib[f]), splat(-kLog2e)));
+    float2 rr, gg, ev, a, s, is;
+    sigmoid2(make_float2(min_nan(t.x, 60.f), min_nan(t.y, 60.f)), make_float2(min_nan(n.x, 60.f), min_nan(n.y, 60.f)), rr, gg, ev);
+    decay<false>(fma2(make_float2(decay_rate(p.c, lam[e]), decay_rate(p.c, lam[f])), rr, splat(kTiny)), a, s, is);
+    const float2 in = mul2(mul2(mul2(s, is), gg), make_float2(to_f32(x[e]), to_f32(x[f])));
+    const float2 hn = fma2(a, make_float2(h[e], h[f]), in);
+    h[e] = hn.x;
+    h[f] = hn.y;
+    o[e] = from_f32<Tout>(hn.x);
+    o[f] = from_f32<Tout>(hn.y);
   }
   if constexpr (V == 4) {
     using O4 = typename std::conditional<sizeof(Tout) == 4, float4, uint2>::type;
@@ -512,7 +728,7 @@ namespace {
 // Warps per row: one where the rows alone give every SM enough warps to hide the memory latency
 // (kWantWarps in flight on the whole GPU), else the fewest of 4, 8, 16 that do, and never many more
 // than the row has chunks.
-constexpr int64_t kWantWarps = 148 * 24;
+constexpr int64_t kWantWarps = 148 * 8;
 
 int warps_per_row(int64_t rows, int64_t L) {
   const int64_t chunks = (L + 7 + kChunk - 1) / kChunk;
@@ -522,15 +738,20 @@ int warps_per_row(int64_t rows, int64_t L) {
   return w;
 }
 
+// Shared memory beyond the default 48 KB is asked for on the current device, at every launch.
+template <typename K> cudaError_t allow_smem(K kernel, int bytes) {
+  if (bytes <= 47 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <typename T, typename Tout, int W>
 cudaError_t fwd_w(const LruParams &p, cudaStream_t s) {
-  const int64_t rows = p.Bt * p.Dn, blocks = W == 1 ? (rows + 3) / 4 : rows;
+  const int64_t blocks = p.Bt * p.Dn;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int threads = W == 1 ? 128 : 32 * W;
-  if (p.reset)
-    lru_fwd_kernel<T, Tout, W, true><<<(unsigned)blocks, threads, 0, s>>>(p);
-  else
-    lru_fwd_kernel<T, Tout, W, false><<<(unsigned)blocks, threads, 0, s>>>(p);
+  const int smem = W * Ring<T, 3, kStages<T, W>>::kWarpBytes;
+  const auto kernel = p.reset ? lru_fwd_kernel<T, Tout, W, true> : lru_fwd_kernel<T, Tout, W, false>;
+  if (cudaError_t e = allow_smem(kernel, smem)) return e;
+  kernel<<<(unsigned)blocks, 32 * W, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -545,13 +766,12 @@ template <typename T, typename Tout> cudaError_t fwd_t(const LruParams &p, cudaS
 
 template <typename T, typename Tg, int W>
 cudaError_t bwd_w(const LruBwdParams &q, cudaStream_t s) {
-  const int64_t rows = q.f.Bt * q.f.Dn, blocks = W == 1 ? (rows + 3) / 4 : rows;
+  const int64_t blocks = q.f.Bt * q.f.Dn;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int threads = W == 1 ? 128 : 32 * W;
-  if (q.f.reset)
-    lru_bwd_kernel<T, Tg, W, true><<<(unsigned)blocks, threads, 0, s>>>(q);
-  else
-    lru_bwd_kernel<T, Tg, W, false><<<(unsigned)blocks, threads, 0, s>>>(q);
+  const int smem = W * Ring<T, 4, kStages<T, W>>::kWarpBytes;
+  const auto kernel = q.f.reset ? lru_bwd_kernel<T, Tg, W, true> : lru_bwd_kernel<T, Tg, W, false>;
+  if (cudaError_t e = allow_smem(kernel, smem)) return e;
+  kernel<<<(unsigned)blocks, 32 * W, smem, s>>>(q);
   return cudaGetLastError();
 }
 

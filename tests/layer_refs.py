@@ -4,10 +4,10 @@ state-space-dual step, each with a bound on what the kernels' roundings can add,
 eps = 2^-24 is half a step of fp32. The bounds carry the rounding errors of the kernels' formulas forward with
 absolute values in the place of every term, so cancellation is covered:
 
-  * sigmoid: fp32 inputs 3 eps relative; bf16 inputs 20 eps (the exponent's rounding, up to 8 eps for
-    |argument| <= 8, hardware exp2 and reciprocal at 4 and 2 eps, the products).
-  * la = log decay: that plus two products, KL = 8 or 24 eps; a absolutely a |la| KL + eps or less; e^la - 1 and with it
-    1 - a^2 to KL + 8 relative, m = sqrt(1 - a^2) to half of that; b = m g x to KB = 16 or 45.
+  * sigmoid: 20 eps relative (the exponent's rounding, up to 8 eps for |argument| <= 8, hardware exp2 and
+    reciprocal at 4 and 2 eps, the products).
+  * la = log decay: that plus two products, KL = 24 eps; a absolutely a |la| KL + eps or less; e^la - 1 and with it
+    1 - a^2 to KL + 8 relative, m = sqrt(1 - a^2) to half of that; b = m g x to KB = 45.
   * a step of the recurrence adds the errors of a (relative to a |h|, |h| the recurrence over |b|), of b and 2 eps
     for its own rounding; the tree that composes a chunk adds at most 5 shuffle levels, 8 elements and 16 warps.
 """
@@ -43,8 +43,7 @@ def check(name, got, ref, bound):
 
 def lru(x, r, i, lam, r_bias=None, i_bias=None, c=8.0, h0=None, reset=None, lengths=None, dout=None, dh_last=None):
     """Outputs and, with dout, gradients of the recurrence, as {name: (value, bound before the last rounding)}."""
-    fast = x.dtype == torch.bfloat16
-    KL, KB, KG = (24.0, 45.0, 110.0) if fast else (8.0, 16.0, 40.0)
+    KL, KB, KG = 24.0, 45.0, 110.0
     x, r, i, lam = d64(x), d64(r), d64(i), d64(lam)
     Bt, Dn, L = x.shape
     rb = torch.zeros(Dn).double() if r_bias is None else d64(r_bias)
