@@ -143,7 +143,7 @@ ssm_status check_qk(const ssm_qk_args *a, bool bwd, bool *empty) {
   if (a->layout != SSM_QK_STATE_LAST && a->layout != SSM_QK_TIME_LAST) return SSM_ERR_UNSUPPORTED;
   if (!(a->eps >= 0.f) || (!a->norm && (a->q_weight || a->k_weight))) return SSM_ERR_UNSUPPORTED;
   int64_t tokens, heads, elems;
-  if (a->Hq > (1 << 24) || a->Hk > (1 << 24) || !mul_ok(a->Bt, a->L, &tokens) ||
+  if (a->Hq > (1 << 24) || a->Hk > (1 << 24) || a->Bt > 0x7fffffff || a->L > 0x7fffff00 || !mul_ok(a->Bt, a->L, &tokens) ||
       !mul_ok(tokens, a->Hq + a->Hk, &heads) || !mul_ok(heads, a->D, &elems) || elems > kMaxElems || tokens > kMaxElems)
     return SSM_ERR_SHAPE;
   if (!aligned(a->q_weight, 4) || !aligned(a->k_weight, 4) || !aligned(a->inv_freq, a->freq_f64 ? 8 : 4) ||

@@ -13,9 +13,7 @@
 // that both members of a pair are in one unit -- elements [8u, 8u+8) and [rot/2 + 8u, ...) of the
 // half layout, 16 consecutive ones of the interleaved layout and of the unrotated rest -- so the rotation needs
 // no exchange between lanes. G lanes hold a row (G = units rounded up to a power of two) and add
-// its squares by shuffles. A group of lanes takes several heads of one token, queries and keys alike, and
-// computes the token's cosines and sines once for them. Head sizes or alignments that do not fit
-// take the same kernel with units of one pair and a warp per row.
+// its squares by shuffles. Head sizes, strides or alignments that do not fit take units of one pair.
 //
 // Time innermost (time_last): a thread owns consecutive steps (8 where rows are whole 16-byte runs, else 1)
 // of a few pairs; the squares meet in shared memory, and with more than one pair a thread the elements are
@@ -33,7 +31,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThr = 256;                 // threads per CTA
-constexpr int kBwdCtas = 148 * 3;         // CTAs of a backward that keeps sums (three per SM)
+constexpr int kBwdCtas = 148 * 3;         // most CTAs of a backward (each keeps a share of dw)
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 __device__ __forceinline__ float ld1(const void *p, int bf16, int64_t i) {
@@ -59,18 +57,23 @@ __device__ __forceinline__ void st8any(void *p, int bf16, int64_t i, const float
   else st8(static_cast<float *>(p) + i, v);
 }
 
+// Rows asked for ahead, and in use, per group of lanes: 16 KB of slots a CTA in bf16.
+template <typename T, typename Td, bool BWD> constexpr int kRowStages = BWD ? (sizeof(T) + sizeof(Td) <= 4 ? 4 : 3) : (sizeof(T) == 2 ? 4 : 3);
+
 __device__ __forceinline__ double position(const QkParams &p, int64_t b, int64_t t) {
   if (!p.pos) return (double)(p.pos0 + t);
   return p.pos_i64 ? (double)static_cast<const int64_t *>(p.pos)[b * p.L + t]
                    : (double)static_cast<const int32_t *>(p.pos)[b * p.L + t];
 }
+// Turns per position of pair j.
 __device__ __forceinline__ double frequency(const QkParams &p, int j) {
-  return p.freq_f64 ? static_cast<const double *>(p.inv_freq)[j] : (double)static_cast<const float *>(p.inv_freq)[j];
+  return kInvTwoPi *
+         (p.freq_f64 ? static_cast<const double *>(p.inv_freq)[j] : (double)static_cast<const float *>(p.inv_freq)[j]);
 }
-// Cosine and sine of pos * f, times the scale.
+// Cosine and sine of pos * f turns, times the scale.
 template <bool PRECISE>
 __device__ __forceinline__ void turn(double pos, double f, float scale, float &c, float &s) {
-  const double t = pos * f * kInvTwoPi;
+  const double t = pos * f;
   const float frac = (float)(t - rint(t));  // a fraction of a turn in [-1/2, 1/2]
   if (PRECISE) {
     sincospif(2.f * frac, &s, &c);
@@ -87,85 +90,64 @@ template <bool PRECISE> __device__ __forceinline__ float inv_rms(const QkParams 
   return PRECISE ? 1.f / sqrtf(ms) : rsqrtf(ms);
 }
 
-// Unit u of a row, V elements at o1 and V at o2, in pairs when it is one of the `ur` rotated units:
-// (o1 + e, o2 + e) of the half layout; (2 e, 2 e + 1) of the 2 V at o1 of the interleaved one.
-template <int V> struct Unit {
+// Pair unit u of a row: elements o1 and o2, turned as a pair where rot; o2 == D at an odd end.
+struct Unit {
   int o1, o2;
   bool on, rot;
 };
-template <int V> __device__ __forceinline__ Unit<V> unit_of(const QkParams &p, int u) {
-  const int ur = p.rot / (2 * V), n = (p.D - p.rot + 2 * V - 1) / (2 * V);
-  Unit<V> r;
+__device__ __forceinline__ Unit unit_of(const QkParams &p, int u) {
+  const int ur = p.rot / 2, n = (p.D - p.rot + 1) / 2;
+  Unit r;
   r.rot = u < ur;
   r.on = u < ur + n;
   const bool half = r.rot && !p.interleaved;
-  r.o1 = half ? u * V : 2 * V * u;  // the rest follows the rotated units at 2 V u too
-  r.o2 = half ? p.rot / 2 + u * V : r.o1 + V;
+  r.o1 = half ? u : 2 * u;  // the rest follows the rotated pairs at 2 u too
+  r.o2 = half ? ur + u : r.o1 + 1;
   return r;
 }
-
-// Turn the 2 V elements of a rotated unit by its V angles (sign -1: back).
-template <int V>
-__device__ __forceinline__ void turn_unit(const QkParams &p, float *v, const float *c, const float *s, float sign) {
-  if (p.interleaved) {
-#pragma unroll
-    for (int e = 0; e < V; e++) {
-      const float a = v[2 * e], b = v[2 * e + 1], sn = sign * s[e];
-      v[2 * e] = a * c[e] - b * sn;
-      v[2 * e + 1] = b * c[e] + a * sn;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; e++) {
-      const float a = v[e], b = v[V + e], sn = sign * s[e];
-      v[e] = a * c[e] - b * sn;
-      v[V + e] = b * c[e] + a * sn;
-    }
-  }
+__device__ __forceinline__ void load_unit(const void *p, int bf16, int64_t at, const Unit &u, bool on, int D, float *v) {
+  v[0] = u.on && on ? ld1(p, bf16, at + u.o1) : 0.f;
+  v[1] = u.on && on && u.o2 < D ? ld1(p, bf16, at + u.o2) : 0.f;
+}
+__device__ __forceinline__ void store_unit(void *p, int bf16, int64_t at, const Unit &u, bool on, int D, const float *v) {
+  if (!u.on || !on) return;
+  st1(p, bf16, at + u.o1, v[0]);
+  if (u.o2 < D) st1(p, bf16, at + u.o2, v[1]);
+}
+__device__ __forceinline__ void load_weights(const float *w, const Unit &u, int D, float *v) {
+  v[0] = w && u.on ? w[u.o1] : 1.f;
+  v[1] = w && u.on && u.o2 < D ? w[u.o2] : 1.f;
 }
 
-template <int V>
-__device__ __forceinline__ void load_unit(const void *p, int bf16, int64_t at, const Unit<V> &u, int D, float *v) {
-  if constexpr (V == 8) {
-    if (u.on) {
-      ld8any(p, bf16, at + u.o1, v);
-      ld8any(p, bf16, at + u.o2, v + 8);
-    } else {
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+// The 16 elements of a unit as two runs of 8, first and second members of its pairs: the two groups of the
+// half layout, the even and the odd elements of the interleaved one.
+template <bool INTER, typename T> __device__ __forceinline__ void runs(const Raw8<T> &a, const Raw8<T> &b, float2 *f, float2 *s) {
+  float v[16];
+  unpack8(a, v);
+  unpack8(b, v + 8);
 #pragma unroll
-      for (int e = 0; e < 16; e++) v[e] = 0.f;
-    }
-  } else {
-    v[0] = u.on ? ld1(p, bf16, at + u.o1) : 0.f;
-    v[1] = u.on && u.o2 < D ? ld1(p, bf16, at + u.o2) : 0.f;
+  for (int j = 0; j < 4; j++) {
+    f[j] = INTER ? make_float2(v[4 * j], v[4 * j + 2]) : make_float2(v[2 * j], v[2 * j + 1]);
+    s[j] = INTER ? make_float2(v[4 * j + 1], v[4 * j + 3]) : make_float2(v[8 + 2 * j], v[8 + 2 * j + 1]);
   }
 }
-template <int V>
-__device__ __forceinline__ void store_unit(void *p, int bf16, int64_t at, const Unit<V> &u, int D, const float *v) {
-  if (!u.on) return;
-  if constexpr (V == 8) {
-    st8any(p, bf16, at + u.o1, v);
-    st8any(p, bf16, at + u.o2, v + 8);
-  } else {
-    st1(p, bf16, at + u.o1, v[0]);
-    if (u.o2 < D) st1(p, bf16, at + u.o2, v[1]);
-  }
-}
-// The weights of a unit (1 without weights).
-template <int V>
-__device__ __forceinline__ void load_weights(const float *w, const Unit<V> &u, int D, float *v) {
+template <bool INTER>
+__device__ __forceinline__ void store_runs(void *p, int bf16, int64_t o1, int64_t o2, const float2 *f, const float2 *s) {
+  float v[16];
 #pragma unroll
-  for (int e = 0; e < 2 * V; e++) v[e] = 1.f;
-  if (!w || !u.on) return;
-  if constexpr (V == 8) {
-    Raw8<float> r;
-    ld8(w + u.o1, r);
-    unpack8(r, v);
-    ld8(w + u.o2, r);
-    unpack8(r, v + 8);
-  } else {
-    v[0] = w[u.o1];
-    if (u.o2 < D) v[1] = w[u.o2];
+  for (int j = 0; j < 4; j++) {
+    v[INTER ? 4 * j : 2 * j] = f[j].x;
+    v[INTER ? 4 * j + 2 : 2 * j + 1] = f[j].y;
+    v[INTER ? 4 * j + 1 : 8 + 2 * j] = s[j].x;
+    v[INTER ? 4 * j + 3 : 8 + 2 * j + 1] = s[j].y;
   }
+  st8any(p, bf16, o1, v);
+  st8any(p, bf16, o2, v + 8);
 }
 
 // n / d and the remainder, in 32 bits where both fit.
@@ -183,175 +165,383 @@ __device__ __forceinline__ void divide(int64_t n, int64_t d, int64_t &q, int64_t
 
 // ---- head elements innermost -------------------------------------------------------------------
 
-// A group of G lanes takes HP rows (heads; queries first, then keys) of one token. NU units a lane.
-template <typename T, int V, int NU, int HP>
-__global__ void __launch_bounds__(kThr) qk_fwd_kernel(const __grid_constant__ QkParams p, int G, int64_t chunks) {
-  constexpr bool PRECISE = sizeof(T) == 4;
-  const int lane = threadIdx.x & 31, sub = lane % G;
-  const int64_t item = ((int64_t)blockIdx.x * kThr + threadIdx.x) / G;
-  int64_t token, chunk, b, t;
-  divide(item, chunks, token, chunk);
-  divide(token, p.L, b, t);
-  const bool live = b < p.Bt;  // dead groups follow along for the shuffles
-  Unit<V> u[NU];
-#pragma unroll
-  for (int n = 0; n < NU; n++) {
-    u[n] = unit_of<V>(p, sub + n * G);
-    u[n].on = u[n].on && live;
+// Rows (b, t, h) of one side, heads fastest, walked in steps of `step` rows.
+struct Walk {
+  int b, t, h;
+  __device__ __forceinline__ void start(int64_t row, int64_t H, int64_t L) {
+    int64_t token, hh, bb, tt;
+    divide(row, H, token, hh);
+    divide(token, L, bb, tt);
+    b = (int)bb;
+    t = (int)tt;
+    h = (int)hh;
   }
-  const int h0 = (int)chunk * HP;
-  float v[HP][NU][2 * V];
-#pragma unroll
-  for (int k = 0; k < HP; k++) {
-    const int h = h0 + k, side = h >= p.H[0];
-    const bool on = h < p.H[0] + p.H[1];
-    const QkTensor &in = p.in[side];
-    const int64_t at = b * in.sb + t * in.sr + (h - (side ? p.H[0] : 0)) * in.sh;
-#pragma unroll
-    for (int n = 0; n < NU; n++) {
-      Unit<V> un = u[n];
-      un.on = un.on && on;
-      load_unit<V>(in.p, PRECISE ? 0 : 1, at, un, p.D, v[k][n]);
+  // dt = step / H, dh = step % H; true where the token changed.
+  __device__ __forceinline__ bool advance(int dt, int dh, int H, int L) {
+    h += dh;
+    const int more = h >= H;
+    if (more) h -= H;
+    t += dt + more;
+    while (t >= L) {
+      t -= L;
+      b++;
     }
+    return dt + more != 0;
   }
-  float c[NU][V], s[NU][V];
-  const double pos = live && p.rot ? position(p, b, t) : 0.0;
-#pragma unroll
-  for (int n = 0; n < NU; n++)
-    if (u[n].on && u[n].rot) {
-#pragma unroll
-      for (int e = 0; e < V; e++) turn<PRECISE>(pos, frequency(p, (sub + n * G) * V + e), p.rot_scale, c[n][e], s[n][e]);
-    }
-#pragma unroll
-  for (int k = 0; k < HP; k++) {
-    const int h = h0 + k, side = h >= p.H[0];
-    const bool on = h < p.H[0] + p.H[1];
-    if (p.norm) {
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < NU; n++)
-#pragma unroll
-        for (int e = 0; e < 2 * V; e++) sum = fmaf(v[k][n][e], v[k][n][e], sum);
-      for (int off = G / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-      const float sc = inv_rms<PRECISE>(p, sum);
-#pragma unroll
-      for (int n = 0; n < NU; n++) {
-        float w[2 * V];
-        load_weights<V>(p.w[side], u[n], p.D, w);
-#pragma unroll
-        for (int e = 0; e < 2 * V; e++) v[k][n][e] *= sc * w[e];
-      }
-    }
-    const QkTensor &out = p.out[side];
-    const int64_t at = b * out.sb + t * out.sr + (h - (side ? p.H[0] : 0)) * out.sh;
-#pragma unroll
-    for (int n = 0; n < NU; n++) {
-      if (u[n].rot) turn_unit<V>(p, v[k][n], c[n], s[n], 1.f);
-      Unit<V> un = u[n];
-      un.on = un.on && on;
-      store_unit<V>(out.p, out.bf16, at, un, p.D, v[k][n]);
-    }
-  }
-}
+  __device__ __forceinline__ int64_t at(const QkTensor &x) const { return b * x.sb + t * x.sr + h * x.sh; }
+};
 
-// Groups of lanes walk the rows of one side (blocks [0, nb0) the queries, the others the keys) with a stride
-// of the side's groups, HP heads of a token at a time, and keep their share of dw in registers.
-template <typename T, int V, int NU, int HP>
-__global__ void __launch_bounds__(kThr) qk_bwd_kernel(const __grid_constant__ QkParams p, int G, int nb0) {
+// Rows in 16-byte runs. CTAs [0, nb0) take the queries, the others the keys; a warp takes `per` consecutive rows
+// of its side, 32 / G at a time (G lanes a row, a unit of 16 elements each), and the rows ahead travel in a ring of
+// cp.async slots that every lane fills and reads alone. Cosines and sines are recomputed where the token
+// changes; a unit that is not rotated keeps 1 and 0. The backward adds its share of dw over all its rows.
+template <typename T, typename Td, bool BWD, bool INTER>
+__global__ void __launch_bounds__(kThr, BWD ? 2 : 3)
+qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0, int64_t per1) {
   constexpr bool PRECISE = sizeof(T) == 4;
-  extern __shared__ float sdw[];  // (groups, D) with dw
+  constexpr int kSlotsV = sizeof(T), kSlotsG = BWD ? sizeof(Td) : 0;  // 16-byte slots of 16 elements
+  constexpr int kSlots = kSlotsV + kSlotsG;
+  constexpr int S = kRowStages<T, Td, BWD>;
+  extern __shared__ __align__(16) char smem[];  // the ring; afterwards (groups, D) sums of dw
   const int side = (int)blockIdx.x >= nb0;
-  const int64_t block = side ? blockIdx.x - nb0 : blockIdx.x, blocks = side ? gridDim.x - nb0 : nb0;
-  const int lane = threadIdx.x & 31, sub = lane % G, per_cta = kThr / G;
-  const int64_t chunks = (p.H[side] + HP - 1) / HP, items = p.Bt * p.L * chunks;
+  const int block = side ? blockIdx.x - nb0 : blockIdx.x;
+  const int lane = threadIdx.x & 31, sub = lane & (G - 1), grp = lane / G, step = 32 / G;
+  const int64_t per = side ? per1 : per0;
+  const int H = p.H[side], L = (int)p.L;
   const QkTensor in = p.in[side], dout = p.dout[side], out = p.out[side];
-  Unit<V> u[NU];
-  float w[NU][2 * V], dw[NU][2 * V];
+  const int64_t first = ((int64_t)block * (kThr / 32) + (threadIdx.x >> 5)) * per;
+  const int64_t total = p.Bt * p.L * H;
+  const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
+  const int dt = step / H, dh = step % H;
+  // the lane's unit
+  const int ur = p.rot / 16;
+  const bool on = sub < p.D / 16, rot = sub < ur;
+  const bool half = rot && !INTER;
+  const int o1 = half ? 8 * sub : 16 * sub, o2 = half ? p.rot / 2 + 8 * sub : o1 + 8;
+  // in shared memory, by unit: the weights of its two runs, and its pairs' turns per position
+  __shared__ float4 sw[4][32];
+  __shared__ double sf[8][32];
+  if (threadIdx.x < p.D / 16) {
+    float2 w[8];
 #pragma unroll
-  for (int n = 0; n < NU; n++) {
-    u[n] = unit_of<V>(p, sub + n * G);
-    if (p.norm) load_weights<V>(p.w[side], u[n], p.D, w[n]);
+    for (int j = 0; j < 8; j++) w[j] = splat(1.f);
+    if (p.norm && p.w[side]) {
+      const int u = threadIdx.x;
+      const bool h = u < ur && !INTER;
+      Raw8<float> a, b;
+      ld8(p.w[side] + (h ? 8 * u : 16 * u), a);
+      ld8(p.w[side] + (h ? p.rot / 2 + 8 * u : 16 * u + 8), b);
+      runs<INTER>(a, b, w, w + 4);
+    }
 #pragma unroll
-    for (int e = 0; e < 2 * V; e++) dw[n][e] = 0.f;
+    for (int j = 0; j < 4; j++) sw[j][threadIdx.x] = make_float4(w[2 * j].x, w[2 * j].y, w[2 * j + 1].x, w[2 * j + 1].y);
   }
-  const int64_t stride = blocks * per_cta;
-  // the trip count is the block's, so that every lane of a warp is there for the shuffles
-  for (int64_t i0 = block * per_cta; i0 < items; i0 += stride) {
-    const int64_t item = i0 + threadIdx.x / G;
-    const bool live = item < items;
-    int64_t token, chunk, b, t;
-    divide(live ? item : 0, chunks, token, chunk);
-    divide(token, p.L, b, t);
-    float v[HP][NU][2 * V], g[HP][NU][2 * V];
+  for (int j = threadIdx.x; j < p.rot / 2; j += kThr) sf[j & 7][j >> 3] = frequency(p, j);
+  float2 d1[4], d2[4], c[4], s[4];
 #pragma unroll
-    for (int k = 0; k < HP; k++) {
-      const int64_t h = chunk * HP + k;
+  for (int j = 0; j < 4; j++) {
+    d1[j] = d2[j] = s[j] = splat(0.f);
+    c[j] = splat(1.f);
+  }
+  char *const mine = smem + threadIdx.x * 16;
+  auto slot = [&](int stage, int k) { return mine + (stage * kSlots + k) * (kThr * 16); };
+  Walk ahead, now;
+  ahead.start(first + grp, H, L);
+  now = ahead;
+  int left = n_rows - grp;  // rows of this group still to be asked for, times step
+  auto fetch = [&](int stage) {
+    if (left > 0 && on) {
+      if (!BWD || p.norm) {
+        const char *a = reinterpret_cast<const char *>(static_cast<const T *>(in.p) + ahead.at(in));
 #pragma unroll
-      for (int n = 0; n < NU; n++) {
-        Unit<V> un = u[n];
-        un.on = un.on && live && h < p.H[side];
-        load_unit<V>(dout.p, dout.bf16, b * dout.sb + t * dout.sr + h * dout.sh, un, p.D, g[k][n]);
-        if (p.norm) load_unit<V>(in.p, PRECISE ? 0 : 1, b * in.sb + t * in.sr + h * in.sh, un, p.D, v[k][n]);
+        for (int k = 0; k < kSlotsV / 2; k++) {
+          cp_async16(slot(stage, k), a + o1 * sizeof(T) + 16 * k);
+          cp_async16(slot(stage, kSlotsV / 2 + k), a + o2 * sizeof(T) + 16 * k);
+        }
+      }
+      if (BWD) {
+        const char *a = reinterpret_cast<const char *>(static_cast<const Td *>(dout.p) + ahead.at(dout));
+#pragma unroll
+        for (int k = 0; k < kSlotsG / 2; k++) {
+          cp_async16(slot(stage, kSlotsV + k), a + o1 * sizeof(Td) + 16 * k);
+          cp_async16(slot(stage, kSlotsV + kSlotsG / 2 + k), a + o2 * sizeof(Td) + 16 * k);
+        }
       }
     }
-    const double pos = p.rot ? position(p, b, t) : 0.0;
+    left -= step;
+    ahead.advance(dt, dh, H, L);
+    cp_async_commit();
+  };
+  auto take = [&](int stage, int k, auto &a, auto &b) {
+    constexpr int n = sizeof(a) / 16;
 #pragma unroll
-    for (int n = 0; n < NU; n++)
-      if (u[n].on && u[n].rot) {
-        float c[V], s[V];
+    for (int j = 0; j < n; j++) {
+      reinterpret_cast<uint4 *>(&a)[j] = *reinterpret_cast<const uint4 *>(slot(stage, k + j));
+      reinterpret_cast<uint4 *>(&b)[j] = *reinterpret_cast<const uint4 *>(slot(stage, k + n + j));
+    }
+  };
 #pragma unroll
-        for (int e = 0; e < V; e++) turn<PRECISE>(pos, frequency(p, (sub + n * G) * V + e), p.rot_scale, c[e], s[e]);
+  for (int j = 0; j < S - 1; j++) fetch(j);
+  // the weights of run 1 (pairs 0 .. 3) or 2 (4 .. 7)
+  auto weights = [&](int run, float2 *w) {
+    const float4 a = sw[2 * run][sub], b = sw[2 * run + 1][sub];
+    w[0] = make_float2(a.x, a.y);
+    w[1] = make_float2(a.z, a.w);
+    w[2] = make_float2(b.x, b.y);
+    w[3] = make_float2(b.z, b.w);
+  };
+  __syncthreads();
+  int stage = 0;
+  bool fresh = true;
+  for (int i = 0; i < n_rows; i += step) {
+    const bool live = i + grp < n_rows;
+    fetch(stage == 0 ? S - 1 : stage - 1);
+    if (fresh && rot && on && live) {
+      const double pos = position(p, now.b, now.t);
 #pragma unroll
-        for (int k = 0; k < HP; k++) turn_unit<V>(p, g[k][n], c, s, -1.f);
+      for (int j = 0; j < 4; j++) {
+        turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
+        turn<PRECISE>(pos, sf[2 * j + 1][sub], p.rot_scale, c[j].y, s[j].y);
+      }
+    }
+    cp_async_wait<S - 1>();
+    float2 v1[4], v2[4];
+    if (!BWD || p.norm) {
+      Raw8<T> a, b;
+      take(stage, 0, a, b);
+      runs<INTER>(a, b, v1, v2);
+      if (!on || !live) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v1[j] = v2[j] = splat(0.f);
+      }
+    }
+    if constexpr (BWD) {
+      float2 g1[4], g2[4];
+      {
+        Raw8<Td> a, b;
+        take(stage, kSlotsV, a, b);
+        runs<INTER>(a, b, g1, g2);
       }
 #pragma unroll
-    for (int k = 0; k < HP; k++) {
-      const int64_t h = chunk * HP + k;
+      for (int j = 0; j < 4; j++) {
+        const float2 x = g1[j], y = g2[j];
+        g1[j] = fma2(y, s[j], mul2(x, c[j]));
+        g2[j] = fma2(x, neg2(s[j]), mul2(y, c[j]));
+      }
       if (p.norm) {
-        float sum = 0.f, dot = 0.f;
+        if (!on || !live) {
 #pragma unroll
-        for (int n = 0; n < NU; n++)
+          for (int j = 0; j < 4; j++) g1[j] = g2[j] = splat(0.f);
+        }
+        float2 s2 = splat(0.f), t2 = splat(0.f), gw1[4], gw2[4];
+        weights(0, gw1);
+        weights(1, gw2);
 #pragma unroll
-          for (int e = 0; e < 2 * V; e++) {
-            sum = fmaf(v[k][n][e], v[k][n][e], sum);
-            dot = fmaf(g[k][n][e] * w[n][e], v[k][n][e], dot);
-          }
+        for (int j = 0; j < 4; j++) {
+          gw1[j] = mul2(g1[j], gw1[j]);
+          gw2[j] = mul2(g2[j], gw2[j]);
+          s2 = fma2(v1[j], v1[j], s2);
+          s2 = fma2(v2[j], v2[j], s2);
+          t2 = fma2(gw1[j], v1[j], t2);
+          t2 = fma2(gw2[j], v2[j], t2);
+        }
+        float sum = s2.x + s2.y, dot = t2.x + t2.y;
         for (int off = G / 2; off >= 1; off >>= 1) {
           sum += __shfl_xor_sync(kFull, sum, off);
           dot += __shfl_xor_sync(kFull, dot, off);
         }
         const float sc = inv_rms<PRECISE>(p, sum);
-        const float back = sc * sc * dot * p.inv_D;
+        const float2 k2 = splat(-sc * sc * sc * dot * p.inv_D), sc2 = splat(sc);
 #pragma unroll
-        for (int n = 0; n < NU; n++)
-#pragma unroll
-          for (int e = 0; e < 2 * V; e++) {
-            dw[n][e] = fmaf(g[k][n][e] * sc, v[k][n][e], dw[n][e]);
-            g[k][n][e] = sc * (g[k][n][e] * w[n][e] - v[k][n][e] * back);
-          }
-      }
-      if (out.p) {
-#pragma unroll
-        for (int n = 0; n < NU; n++) {
-          Unit<V> un = u[n];
-          un.on = un.on && live && h < p.H[side];
-          store_unit<V>(out.p, out.bf16, b * out.sb + t * out.sr + h * out.sh, un, p.D, g[k][n]);
+        for (int j = 0; j < 4; j++) {
+          d1[j] = fma2(mul2(g1[j], sc2), v1[j], d1[j]);
+          d2[j] = fma2(mul2(g2[j], sc2), v2[j], d2[j]);
+          g1[j] = fma2(v1[j], k2, mul2(gw1[j], sc2));
+          g2[j] = fma2(v2[j], k2, mul2(gw2[j], sc2));
         }
       }
+      if (out.p && on && live) {
+        const int64_t at = now.at(out);
+        store_runs<INTER>(out.p, out.bf16, at + o1, at + o2, g1, g2);
+      }
+    } else {
+      if (p.norm) {
+        float2 s2 = splat(0.f);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          s2 = fma2(v1[j], v1[j], s2);
+          s2 = fma2(v2[j], v2[j], s2);
+        }
+        float sum = s2.x + s2.y;
+        for (int off = G / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+        const float2 sc2 = splat(inv_rms<PRECISE>(p, sum));
+        float2 w[4];
+        weights(0, w);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v1[j] = mul2(v1[j], mul2(w[j], sc2));
+        weights(1, w);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v2[j] = mul2(v2[j], mul2(w[j], sc2));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const float2 x = v1[j], y = v2[j];
+        v1[j] = fma2(y, neg2(s[j]), mul2(x, c[j]));
+        v2[j] = fma2(x, s[j], mul2(y, c[j]));
+      }
+      if (on && live) {
+        const int64_t at = now.at(out);
+        store_runs<INTER>(out.p, out.bf16, at + o1, at + o2, v1, v2);
+      }
+    }
+    stage = stage == S - 1 ? 0 : stage + 1;
+    fresh = now.advance(dt, dh, H, L);
+  }
+  if (!BWD || !p.dw[side]) return;
+  // the block's share of dw: the groups' in their order
+  cp_async_wait<0>();
+  __syncthreads();
+  float *const sums = reinterpret_cast<float *>(smem);
+  if (on) {
+    float *row = sums + (threadIdx.x / G) * p.D;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      row[INTER ? o1 + 4 * j : o1 + 2 * j] = d1[j].x;
+      row[INTER ? o1 + 4 * j + 2 : o1 + 2 * j + 1] = d1[j].y;
+      row[INTER ? o1 + 4 * j + 1 : o2 + 2 * j] = d2[j].x;
+      row[INTER ? o1 + 4 * j + 3 : o2 + 2 * j + 1] = d2[j].y;
+    }
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < p.D; j += kThr) {
+    float t = 0.f;
+    for (int r = 0; r < kThr / G; r++) t += sums[r * p.D + j];
+    p.part[(int64_t)blockIdx.x * p.D + j] = t;
+  }
+}
+
+// Any head size, stride and alignment: units of one pair, NU a lane. G lanes take a row at a time.
+template <typename T, int NU>
+__global__ void __launch_bounds__(kThr) qk_pairs_fwd_kernel(const __grid_constant__ QkParams p, int G) {
+  constexpr bool PRECISE = sizeof(T) == 4;
+  const int lane = threadIdx.x & 31, sub = lane & (G - 1);
+  const int64_t heads = p.H[0] + p.H[1], item = ((int64_t)blockIdx.x * kThr + threadIdx.x) / G;
+  int64_t token, h, b, t;
+  divide(item, heads, token, h);
+  divide(token, p.L, b, t);
+  const bool live = b < p.Bt;  // dead groups follow along for the shuffles
+  const int side = h >= p.H[0];
+  if (side) h -= p.H[0];
+  const QkTensor &in = p.in[side], &out = p.out[side];
+  const int64_t at = b * in.sb + t * in.sr + h * in.sh, to = b * out.sb + t * out.sr + h * out.sh;
+  float v[NU][2], sum = 0.f;
+#pragma unroll
+  for (int n = 0; n < NU; n++) {
+    load_unit(in.p, PRECISE ? 0 : 1, at, unit_of(p, sub + n * G), live, p.D, v[n]);
+    sum = fmaf(v[n][0], v[n][0], fmaf(v[n][1], v[n][1], sum));
+  }
+  const double pos = live && p.rot ? position(p, b, t) : 0.0;
+  if (p.norm) {
+    for (int off = G / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+    sum = inv_rms<PRECISE>(p, sum);
+  }
+#pragma unroll
+  for (int n = 0; n < NU; n++) {
+    const Unit u = unit_of(p, sub + n * G);
+    if (p.norm) {
+      float w[2];
+      load_weights(p.w[side], u, p.D, w);
+      v[n][0] *= sum * w[0];
+      v[n][1] *= sum * w[1];
+    }
+    if (u.rot) {
+      float c, s;
+      turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c, s);
+      const float x = v[n][0], y = v[n][1];
+      v[n][0] = x * c - y * s;
+      v[n][1] = y * c + x * s;
+    }
+    store_unit(out.p, out.bf16, to, u, live, p.D, v[n]);
+  }
+}
+
+// Groups of lanes walk the rows of one side (blocks [0, nb0) the queries, the others the keys) with a stride
+// of the side's groups and keep their share of dw in registers.
+template <typename T, int NU>
+__global__ void __launch_bounds__(kThr) qk_pairs_bwd_kernel(const __grid_constant__ QkParams p, int G, int nb0) {
+  constexpr bool PRECISE = sizeof(T) == 4;
+  extern __shared__ float sdw[];  // (groups, D) with dw
+  const int side = (int)blockIdx.x >= nb0;
+  const int64_t block = side ? blockIdx.x - nb0 : blockIdx.x, blocks = side ? gridDim.x - nb0 : nb0;
+  const int lane = threadIdx.x & 31, sub = lane & (G - 1), per_cta = kThr / G;
+  const int64_t items = p.Bt * p.L * p.H[side];
+  const QkTensor in = p.in[side], dout = p.dout[side], out = p.out[side];
+  float w[NU][2], dw[NU][2];
+#pragma unroll
+  for (int n = 0; n < NU; n++) {
+    if (p.norm) load_weights(p.w[side], unit_of(p, sub + n * G), p.D, w[n]);
+    dw[n][0] = dw[n][1] = 0.f;
+  }
+  // the trip count is the block's, so that every lane of a warp is there for the shuffles
+  for (int64_t i0 = block * per_cta; i0 < items; i0 += blocks * per_cta) {
+    const int64_t item = i0 + threadIdx.x / G;
+    const bool live = item < items;
+    int64_t token, h, b, t;
+    divide(live ? item : 0, p.H[side], token, h);
+    divide(token, p.L, b, t);
+    float v[NU][2], g[NU][2], sum = 0.f, dot = 0.f;
+    const int64_t gat = b * dout.sb + t * dout.sr + h * dout.sh, at = b * in.sb + t * in.sr + h * in.sh;
+#pragma unroll
+    for (int n = 0; n < NU; n++) {
+      const Unit u = unit_of(p, sub + n * G);
+      load_unit(dout.p, dout.bf16, gat, u, live, p.D, g[n]);
+      if (p.norm) load_unit(in.p, PRECISE ? 0 : 1, at, u, live, p.D, v[n]);
+    }
+    const double pos = p.rot ? position(p, b, t) : 0.0;
+#pragma unroll
+    for (int n = 0; n < NU; n++) {
+      if (unit_of(p, sub + n * G).rot) {
+        float c, s;
+        turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c, s);
+        const float x = g[n][0], y = g[n][1];
+        g[n][0] = x * c + y * s;
+        g[n][1] = y * c - x * s;
+      }
+      if (p.norm) {
+        sum = fmaf(v[n][0], v[n][0], fmaf(v[n][1], v[n][1], sum));
+        dot = fmaf(g[n][0] * w[n][0], v[n][0], fmaf(g[n][1] * w[n][1], v[n][1], dot));
+      }
+    }
+    if (p.norm) {
+      for (int off = G / 2; off >= 1; off >>= 1) {
+        sum += __shfl_xor_sync(kFull, sum, off);
+        dot += __shfl_xor_sync(kFull, dot, off);
+      }
+      const float sc = inv_rms<PRECISE>(p, sum), back = sc * sc * dot * p.inv_D;
+#pragma unroll
+      for (int n = 0; n < NU; n++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          dw[n][e] = fmaf(g[n][e] * sc, v[n][e], dw[n][e]);
+          g[n][e] = sc * (g[n][e] * w[n][e] - v[n][e] * back);
+        }
+    }
+    if (out.p) {
+      const int64_t to = b * out.sb + t * out.sr + h * out.sh;
+#pragma unroll
+      for (int n = 0; n < NU; n++) store_unit(out.p, out.bf16, to, unit_of(p, sub + n * G), live, p.D, g[n]);
     }
   }
   if (!p.dw[side]) return;
   // the block's share of dw: the groups' in their order
 #pragma unroll
-  for (int n = 0; n < NU; n++)
-    if (u[n].on) {
-      float *row = sdw + (threadIdx.x / G) * p.D;
-#pragma unroll
-      for (int e = 0; e < V; e++) {
-        row[u[n].o1 + e] = dw[n][e];
-        if (V == 8 || u[n].o2 < p.D) row[u[n].o2 + e] = dw[n][V + e];
-      }
-    }
+  for (int n = 0; n < NU; n++) {
+    const Unit u = unit_of(p, sub + n * G);
+    if (!u.on) continue;
+    float *row = sdw + (threadIdx.x / G) * p.D;
+    row[u.o1] = dw[n][0];
+    if (u.o2 < p.D) row[u.o2] = dw[n][1];
+  }
   __syncthreads();
   for (int j = threadIdx.x; j < p.D; j += kThr) {
     float s = 0.f;
@@ -363,7 +553,7 @@ __global__ void __launch_bounds__(kThr) qk_bwd_kernel(const __grid_constant__ Qk
 // ---- time innermost ----------------------------------------------------------------------------
 
 // TX threads over time, TV steps each, TY = kThr / TX over the pairs of a head, NS pairs a thread.
-// A pair unit is unit_of<1>: elements o1 and o2 (or o1 alone at an odd end).
+// A pair unit is unit_of: elements o1 and o2 (or o1 alone at an odd end).
 template <typename T, int TV> struct TimeLoad {
   static __device__ __forceinline__ void get(const void *p, int bf16, int64_t i, int n, float *v) {
     if constexpr (TV == 8) {
@@ -421,7 +611,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
 #pragma unroll
     for (int e = 0; e < TV; e++) sum[e] = dot[e] = 0.f;
     // the elements of pair unit u, its gradients turned back
-    auto fetch = [&](const Unit<1> &u, int unit) {
+    auto fetch = [&](const Unit &u, int unit) {
       const bool two = u.o2 < p.D;
       if (!BWD || p.norm) {
         M::get(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m, a);
@@ -451,7 +641,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
       for (int n = 0; n < NS; n++) {
         const int unit = ty + n * TY;
         if (unit < n_units) {
-          const Unit<1> u = unit_of<1>(p, unit);
+          const Unit u = unit_of(p, unit);
           fetch(u, unit);
           const float wa = BWD ? weight(u.o1) : 0.f, wc = BWD && u.o2 < p.D ? weight(u.o2) : 0.f;
 #pragma unroll
@@ -484,7 +674,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
     for (int n = 0; n < NS; n++) {
       const int unit = ty + n * TY;
       if (unit < n_units) {
-        const Unit<1> u = unit_of<1>(p, unit);
+        const Unit u = unit_of(p, unit);
         const bool two = u.o2 < p.D;
         if (NS > 1 || !p.norm) fetch(u, unit);  // with one pair it is still here
         const float wa = p.norm ? weight(u.o1) : 1.f, wc = p.norm && two ? weight(u.o2) : 1.f;
@@ -531,7 +721,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
     __syncthreads();
     const int unit = ty + n * TY;
     if (tx == 0 && unit < n_units) {
-      const Unit<1> u = unit_of<1>(p, unit);
+      const Unit u = unit_of(p, unit);
       float x = 0.f, y = 0.f;
       for (int k = 0; k < TX; k++) {
         x += sh[2 * (ty * TX + k)];
@@ -570,10 +760,10 @@ int pow2_at_least(int n) {
   return g;
 }
 
-// Lanes that hold a row with units of 2 V elements, at most a warp.
-int lanes_per_row(const QkParams &p, int V) {
-  const int units = p.rot / (2 * V) + (p.D - p.rot + 2 * V - 1) / (2 * V);
-  const int g = pow2_at_least(units);
+// Lanes that hold a row: a unit of 16 elements each (vec); at least a fourth of the pairs otherwise, at most a warp.
+int lanes_per_row(const QkParams &p) {
+  if (p.vec) return pow2_at_least(p.D / 16);
+  const int pairs = p.rot / 2 + (p.D - p.rot + 1) / 2, g = pow2_at_least((pairs + 3) / 4);
   return g < 32 ? g : 32;
 }
 
@@ -596,9 +786,10 @@ TimePlan time_plan(const QkParams &p) {
   return t;
 }
 
-// CTAs of the backward: in proportion to the rows of a side, at least one where it has any.
-void bwd_blocks(const QkParams &p, const int64_t *work, int *nb0, int *nb1) {
-  const int64_t all = work[0] + work[1], most = all < kBwdCtas ? all : kBwdCtas;
+// At most `most` CTAs over both sides, in proportion to their work (in CTAs), at least one where a side has any.
+void split_blocks(const int64_t *work, int64_t most, int *nb0, int *nb1) {
+  const int64_t all = work[0] + work[1];
+  if (all < most) most = all;
   int64_t n[2];
   for (int s = 0; s < 2; s++) {
     n[s] = all ? work[s] * most / all : 0;
@@ -608,35 +799,59 @@ void bwd_blocks(const QkParams &p, const int64_t *work, int *nb0, int *nb1) {
   *nb1 = (int)n[1];
 }
 
-// Heads per step of a backward's group: two where a side has two.
-int bwd_heads(const QkParams &p) { return p.H[0] > 1 && p.H[1] != 1 ? 2 : 1; }
-
-void bwd_plan(const QkParams &p, int *nb0, int *nb1, int *G, TimePlan *tp) {
-  int64_t work[2];
-  if (p.time_last) {
-    *tp = time_plan(p);
-    work[0] = tp->tiles[0];
-    work[1] = tp->tiles[1];
-  } else {
-    *G = lanes_per_row(p, p.vec ? 8 : 1);
-    const int per_cta = kThr / *G, hp = p.vec ? bwd_heads(p) : 1;
-    for (int s = 0; s < 2; s++) work[s] = (p.Bt * p.L * ((p.H[s] + hp - 1) / hp) + per_cta - 1) / per_cta;
+template <typename T, typename Td, bool BWD, bool INTER>
+cudaError_t rows_launch(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
+  constexpr int kWarps = kThr / 32;
+  const int G = lanes_per_row(p), step = 32 / G;
+  int64_t rows[2], work[2], per[2] = {1, 1};
+  for (int j = 0; j < 2; j++) {
+    rows[j] = p.Bt * p.L * p.H[j];
+    work[j] = (rows[j] + kWarps * step - 1) / (kWarps * step);
   }
-  bwd_blocks(p, work, nb0, nb1);
+  int n[2];
+  split_blocks(work, 148 * (BWD ? 2 : 3), &n[0], &n[1]);
+  for (int j = 0; j < 2; j++) {  // rows per warp, whole steps
+    if (!n[j]) continue;
+    per[j] = (rows[j] + (int64_t)n[j] * kWarps - 1) / ((int64_t)n[j] * kWarps);
+    per[j] = (per[j] + step - 1) / step * step;
+    if (per[j] > 0x7fffff00) return cudaErrorInvalidConfiguration;
+  }
+  *nb0 = n[0];
+  *nb = n[0] + n[1];
+  constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
+  const int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>, sums = (int)sizeof(float) * (kThr / G) * p.D;
+  const int smem = BWD && sums > ring ? sums : ring;
+  const auto kernel = qk_rows_kernel<T, Td, BWD, INTER>;
+  if (smem > 47 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<*nb, kThr, smem, s>>>(p, G, n[0], per[0], per[1]);
+  return cudaGetLastError();
 }
 
-template <typename T, int V, int NU, int HP>
-cudaError_t fwd_launch(const QkParams &p, cudaStream_t s) {
-  const int G = lanes_per_row(p, V);
-  const int64_t chunks = (p.H[0] + p.H[1] + HP - 1) / HP, groups = p.Bt * p.L * chunks;
-  const int64_t blocks = (groups * G + kThr - 1) / kThr;
+template <typename T, int NU> cudaError_t pairs_fwd(const QkParams &p, cudaStream_t s) {
+  const int G = lanes_per_row(p);
+  const int64_t blocks = (p.Bt * p.L * (p.H[0] + p.H[1]) * G + kThr - 1) / kThr;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  qk_fwd_kernel<T, V, NU, HP><<<(unsigned)blocks, kThr, 0, s>>>(p, G, chunks);
+  qk_pairs_fwd_kernel<T, NU><<<(unsigned)blocks, kThr, 0, s>>>(p, G);
+  return cudaGetLastError();
+}
+
+template <typename T, int NU> cudaError_t pairs_bwd(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
+  const int G = lanes_per_row(p), per_cta = kThr / G;
+  int64_t work[2];
+  for (int j = 0; j < 2; j++) work[j] = (p.Bt * p.L * p.H[j] + per_cta - 1) / per_cta;
+  int nb1;
+  split_blocks(work, kBwdCtas, nb0, &nb1);
+  *nb = *nb0 + nb1;
+  const size_t smem = p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)per_cta * p.D : 0;
+  qk_pairs_bwd_kernel<T, NU><<<*nb, kThr, smem, s>>>(p, G, *nb0);
   return cudaGetLastError();
 }
 
 template <typename T, int TV, int NS>
-cudaError_t fwd_time(const QkParams &p, cudaStream_t s) {
+cudaError_t time_fwd(const QkParams &p, cudaStream_t s) {
   const TimePlan t = time_plan(p);
   const int64_t tiles = t.tiles[0] + t.tiles[1];
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -645,53 +860,43 @@ cudaError_t fwd_time(const QkParams &p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T> cudaError_t fwd_t(const QkParams &p, cudaStream_t s) {
-  if (p.time_last) {
-    const bool one = p.rot / 2 + (p.D - p.rot + 1) / 2 <= 32;
-    if (p.vec) return one ? fwd_time<T, 8, 1>(p, s) : fwd_time<T, 8, 8>(p, s);
-    return one ? fwd_time<T, 1, 1>(p, s) : fwd_time<T, 1, 8>(p, s);
-  }
-  if (!p.vec) {
-    const bool few = p.rot / 2 + (p.D - p.rot + 1) / 2 <= 64;
-    return few ? fwd_launch<T, 1, 2, 1>(p, s) : fwd_launch<T, 1, 8, 1>(p, s);
-  }
-  // several heads a group share its angles; one where the rows are too few to fill the GPU's warps
-  const int heads = p.H[0] + p.H[1];
-  const int64_t warps = p.Bt * p.L * heads * lanes_per_row(p, 8) / 32;
-  if (heads >= 4 && warps >= 148 * 64) return fwd_launch<T, 8, 1, 4>(p, s);
-  if (heads >= 2 && warps >= 148 * 32) return fwd_launch<T, 8, 1, 2>(p, s);
-  return fwd_launch<T, 8, 1, 1>(p, s);
-}
-
-template <typename T, int V, int NU, int HP>
-cudaError_t bwd_launch(const QkParams &p, int G, int nb0, int nb, cudaStream_t s) {
-  const size_t smem = p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(kThr / G) * p.D : 0;
-  qk_bwd_kernel<T, V, NU, HP><<<nb, kThr, smem, s>>>(p, G, nb0);
-  return cudaGetLastError();
-}
-
 template <typename T, int TV, int NS>
-cudaError_t bwd_time(const QkParams &p, const TimePlan &t, int nb0, int nb, cudaStream_t s) {
-  const size_t smem = sizeof(float) * kThr * (TV == 1 ? 2 : 2 * TV);
-  qk_time_kernel<T, TV, NS, true><<<nb, kThr, smem, s>>>(p, t.TX, nb0, t.tiles[0], t.tiles[1]);
+cudaError_t time_bwd(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
+  const TimePlan t = time_plan(p);
+  int nb1;
+  split_blocks(t.tiles, kBwdCtas, nb0, &nb1);
+  *nb = *nb0 + nb1;
+  const size_t smem = sizeof(float) * kThr * 2 * TV;
+  qk_time_kernel<T, TV, NS, true><<<*nb, kThr, smem, s>>>(p, t.TX, *nb0, t.tiles[0], t.tiles[1]);
   return cudaGetLastError();
+}
+
+template <typename T> cudaError_t fwd_t(const QkParams &p, cudaStream_t s) {
+  const int pairs = p.rot / 2 + (p.D - p.rot + 1) / 2;
+  if (p.time_last) {
+    if (p.vec) return pairs <= 32 ? time_fwd<T, 8, 1>(p, s) : time_fwd<T, 8, 8>(p, s);
+    return pairs <= 32 ? time_fwd<T, 1, 1>(p, s) : time_fwd<T, 1, 8>(p, s);
+  }
+  if (!p.vec) return pairs <= 128 ? pairs_fwd<T, 4>(p, s) : pairs_fwd<T, 8>(p, s);
+  int nb0, nb;
+  return p.interleaved ? rows_launch<T, T, false, true>(p, &nb0, &nb, s) : rows_launch<T, T, false, false>(p, &nb0, &nb, s);
+}
+
+template <typename T, typename Td> cudaError_t bwd_rows(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
+  return p.interleaved ? rows_launch<T, Td, true, true>(p, nb0, nb, s) : rows_launch<T, Td, true, false>(p, nb0, nb, s);
 }
 
 template <typename T> cudaError_t bwd_t(const QkParams &p, cudaStream_t s) {
-  int nb0 = 0, nb1 = 0, G = 1;
-  TimePlan tp;
-  bwd_plan(p, &nb0, &nb1, &G, &tp);
-  const int nb = nb0 + nb1;
+  const int pairs = p.rot / 2 + (p.D - p.rot + 1) / 2;
+  int nb0 = 0, nb = 0;
   cudaError_t e;
   if (p.time_last) {
-    const bool one = p.rot / 2 + (p.D - p.rot + 1) / 2 <= 32;
-    if (p.vec) e = one ? bwd_time<T, 8, 1>(p, tp, nb0, nb, s) : bwd_time<T, 8, 8>(p, tp, nb0, nb, s);
-    else e = one ? bwd_time<T, 1, 1>(p, tp, nb0, nb, s) : bwd_time<T, 1, 8>(p, tp, nb0, nb, s);
+    if (p.vec) e = pairs <= 32 ? time_bwd<T, 8, 1>(p, &nb0, &nb, s) : time_bwd<T, 8, 8>(p, &nb0, &nb, s);
+    else e = pairs <= 32 ? time_bwd<T, 1, 1>(p, &nb0, &nb, s) : time_bwd<T, 1, 8>(p, &nb0, &nb, s);
   } else if (!p.vec) {
-    const bool few = p.rot / 2 + (p.D - p.rot + 1) / 2 <= 64;
-    e = few ? bwd_launch<T, 1, 2, 1>(p, G, nb0, nb, s) : bwd_launch<T, 1, 8, 1>(p, G, nb0, nb, s);
+    e = pairs <= 128 ? pairs_bwd<T, 4>(p, &nb0, &nb, s) : pairs_bwd<T, 8>(p, &nb0, &nb, s);
   } else {
-    e = bwd_heads(p) == 2 ? bwd_launch<T, 8, 1, 2>(p, G, nb0, nb, s) : bwd_launch<T, 8, 1, 1>(p, G, nb0, nb, s);
+    e = p.dout[p.H[0] == 0].bf16 ? bwd_rows<T, __nv_bfloat16>(p, &nb0, &nb, s) : bwd_rows<T, float>(p, &nb0, &nb, s);
   }
   if (e != cudaSuccess || (!p.dw[0] && !p.dw[1])) return e;
   qk_dw_kernel<<<dim3((unsigned)((p.D + 31) / 32), 2), 256, 0, s>>>(p, nb0, nb);
