@@ -60,10 +60,11 @@ __device__ __forceinline__ void st8any(void *p, int bf16, int64_t i, const float
 // Rows asked for ahead, and in use, per group of lanes: 16 KB of slots a CTA in bf16.
 template <typename T, typename Td, bool BWD> constexpr int kRowStages = BWD ? (sizeof(T) + sizeof(Td) <= 4 ? 4 : 3) : (sizeof(T) == 2 ? 4 : 3);
 
-__device__ __forceinline__ double position(const QkParams &p, int64_t b, int64_t t) {
+// Of token b L + t.
+__device__ __forceinline__ double position(const QkParams &p, int64_t token, int64_t t) {
   if (!p.pos) return (double)(p.pos0 + t);
-  return p.pos_i64 ? (double)static_cast<const int64_t *>(p.pos)[b * p.L + t]
-                   : (double)static_cast<const int32_t *>(p.pos)[b * p.L + t];
+  return p.pos_i64 ? (double)static_cast<const int64_t *>(p.pos)[token]
+                   : (double)static_cast<const int32_t *>(p.pos)[token];
 }
 // Turns per position of pair j.
 __device__ __forceinline__ double frequency(const QkParams &p, int j) {
@@ -85,9 +86,10 @@ __device__ __forceinline__ void turn(double pos, double f, float scale, float &c
   c *= scale;
   s *= scale;
 }
-template <bool PRECISE> __device__ __forceinline__ float inv_rms(const QkParams &p, float sum) {
-  const float ms = fmaf(sum, p.inv_D, p.eps);
-  return PRECISE ? 1.f / sqrtf(ms) : rsqrtf(ms);
+__device__ __forceinline__ float inv_rms(const QkParams &p, float sum) {
+  float r;  // 2^-23 of the result at most
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(sum, p.inv_D, p.eps)));
+  return r;
 }
 
 // Pair unit u of a row: elements o1 and o2, turned as a pair where rot; o2 == D at an odd end.
@@ -165,31 +167,57 @@ __device__ __forceinline__ void divide(int64_t n, int64_t d, int64_t &q, int64_t
 
 // ---- head elements innermost -------------------------------------------------------------------
 
-// Rows (b, t, h) of one side, heads fastest, walked in steps of `step` rows.
+// Rows (b, t, h) of one side, heads fastest, walked in steps of dt tokens and dh heads.
 struct Walk {
-  int b, t, h;
-  __device__ __forceinline__ void start(int64_t row, int64_t H, int64_t L) {
-    int64_t token, hh, bb, tt;
+  int64_t token;  // b L + t
+  int t, h;
+  __device__ __forceinline__ void start(int64_t row, int64_t H, int64_t L, int64_t &b) {
+    int64_t hh, tt;
     divide(row, H, token, hh);
-    divide(token, L, bb, tt);
-    b = (int)bb;
+    divide(token, L, b, tt);
     t = (int)tt;
     h = (int)hh;
   }
-  // dt = step / H, dh = step % H; true where the token changed.
-  __device__ __forceinline__ bool advance(int dt, int dh, int H, int L) {
-    h += dh;
-    const int more = h >= H;
-    if (more) h -= H;
-    t += dt + more;
-    while (t >= L) {
-      t -= L;
-      b++;
-    }
-    return dt + more != 0;
-  }
-  __device__ __forceinline__ int64_t at(const QkTensor &x) const { return b * x.sb + t * x.sr + h * x.sh; }
 };
+// A lane's place in one tensor along a walk, moved by additions alone: a step, a step that passes the last head of a
+// token, a step past the last token of a batch element.
+struct Place {
+  int64_t at, step, wrap, turn;
+  __device__ __forceinline__ Place(const QkTensor &x, const Walk &w, int64_t b, int dt, int dh, int H, int L, int o) {
+    at = b * x.sb + w.t * x.sr + w.h * x.sh + o;
+    step = dt * x.sr + dh * x.sh;
+    wrap = x.sr - H * x.sh;
+    turn = x.sb - L * x.sr;
+  }
+};
+// One step; true where the token changed.
+template <typename... P>
+__device__ __forceinline__ bool advance(Walk &w, int dt, int dh, int H, int L, P &...places) {
+  w.h += dh;
+  const bool more = w.h >= H;
+  const int moved = dt + (more ? 1 : 0);
+  w.t += moved;
+  w.token += moved;
+  ((places.at += places.step), ...);
+  if (more) {
+    w.h -= H;
+    ((places.at += places.wrap), ...);
+  }
+  while (w.t >= L) {
+    w.t -= L;
+    ((places.at += places.turn), ...);
+  }
+  return moved != 0;
+}
+// Sums over the G lanes of a row.
+template <typename... F> __device__ __forceinline__ void sum_lanes(int G, F &...v) {
+  if (G == 8) {  // heads of 128
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) ((v += __shfl_xor_sync(kFull, v, off)), ...);
+  } else {
+    for (int off = G / 2; off >= 1; off >>= 1) ((v += __shfl_xor_sync(kFull, v, off)), ...);
+  }
+}
 
 // Rows in 16-byte runs. CTAs [0, nb0) take the queries, the others the keys; a warp takes `per` consecutive rows
 // of its side, 32 / G at a time (G lanes a row, a unit of 16 elements each), and the rows ahead travel in a ring of
@@ -245,31 +273,48 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   }
   char *const mine = smem + threadIdx.x * 16;
   auto slot = [&](int stage, int k) { return mine + (stage * kSlots + k) * (kThr * 16); };
+  auto clear = [&](int stage) {
+#pragma unroll
+    for (int k = 0; k < kSlots; k++) *reinterpret_cast<uint4 *>(slot(stage, k)) = make_uint4(0, 0, 0, 0);
+  };
+  if (!on) {  // lanes without a unit hold zeros throughout
+#pragma unroll
+    for (int j = 0; j < S; j++) clear(j);
+  }
+  const bool reads_v = !BWD || p.norm;
+  const int gap = o2 - o1;
   Walk ahead, now;
-  ahead.start(first + grp, H, L);
+  int64_t b0;
+  ahead.start(first + grp, H, L, b0);
   now = ahead;
+  Place from(in, ahead, b0, dt, dh, H, L, o1), dfrom(dout, ahead, b0, dt, dh, H, L, o1), to(out, now, b0, dt, dh, H, L, o1);
   int left = n_rows - grp;  // rows of this group still to be asked for, times step
   auto fetch = [&](int stage) {
-    if (left > 0 && on) {
-      if (!BWD || p.norm) {
-        const char *a = reinterpret_cast<const char *>(static_cast<const T *>(in.p) + ahead.at(in));
+    if (left > 0) {
+      if (on) {
+        if (reads_v) {
+          const T *a = static_cast<const T *>(in.p) + from.at, *b = a + gap;
 #pragma unroll
-        for (int k = 0; k < kSlotsV / 2; k++) {
-          cp_async16(slot(stage, k), a + o1 * sizeof(T) + 16 * k);
-          cp_async16(slot(stage, kSlotsV / 2 + k), a + o2 * sizeof(T) + 16 * k);
+          for (int k = 0; k < kSlotsV / 2; k++) {
+            cp_async16(slot(stage, k), reinterpret_cast<const char *>(a) + 16 * k);
+            cp_async16(slot(stage, kSlotsV / 2 + k), reinterpret_cast<const char *>(b) + 16 * k);
+          }
+        }
+        if (BWD) {
+          const Td *a = static_cast<const Td *>(dout.p) + dfrom.at, *b = a + gap;
+#pragma unroll
+          for (int k = 0; k < kSlotsG / 2; k++) {
+            cp_async16(slot(stage, kSlotsV + k), reinterpret_cast<const char *>(a) + 16 * k);
+            cp_async16(slot(stage, kSlotsV + kSlotsG / 2 + k), reinterpret_cast<const char *>(b) + 16 * k);
+          }
         }
       }
-      if (BWD) {
-        const char *a = reinterpret_cast<const char *>(static_cast<const Td *>(dout.p) + ahead.at(dout));
-#pragma unroll
-        for (int k = 0; k < kSlotsG / 2; k++) {
-          cp_async16(slot(stage, kSlotsV + k), a + o1 * sizeof(Td) + 16 * k);
-          cp_async16(slot(stage, kSlotsV + kSlotsG / 2 + k), a + o2 * sizeof(Td) + 16 * k);
-        }
-      }
+      left -= step;
+      if (BWD) advance(ahead, dt, dh, H, L, from, dfrom);
+      else advance(ahead, dt, dh, H, L, from);
+    } else {
+      clear(stage);  // behind the group's last row: zeros, which add nothing to dw
     }
-    left -= step;
-    ahead.advance(dt, dh, H, L);
     cp_async_commit();
   };
   auto take = [&](int stage, int k, auto &a, auto &b) {
@@ -296,8 +341,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   for (int i = 0; i < n_rows; i += step) {
     const bool live = i + grp < n_rows;
     fetch(stage == 0 ? S - 1 : stage - 1);
-    if (fresh && rot && on && live) {
-      const double pos = position(p, now.b, now.t);
+    if (fresh && rot && live) {
+      const double pos = position(p, now.token, now.t);
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
@@ -306,14 +351,10 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
     }
     cp_async_wait<S - 1>();
     float2 v1[4], v2[4];
-    if (!BWD || p.norm) {
+    if (reads_v) {
       Raw8<T> a, b;
       take(stage, 0, a, b);
       runs<INTER>(a, b, v1, v2);
-      if (!on || !live) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) v1[j] = v2[j] = splat(0.f);
-      }
     }
     if constexpr (BWD) {
       float2 g1[4], g2[4];
@@ -329,10 +370,6 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
         g2[j] = fma2(x, neg2(s[j]), mul2(y, c[j]));
       }
       if (p.norm) {
-        if (!on || !live) {
-#pragma unroll
-          for (int j = 0; j < 4; j++) g1[j] = g2[j] = splat(0.f);
-        }
         float2 s2 = splat(0.f), t2 = splat(0.f), gw1[4], gw2[4];
         weights(0, gw1);
         weights(1, gw2);
@@ -346,11 +383,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
           t2 = fma2(gw2[j], v2[j], t2);
         }
         float sum = s2.x + s2.y, dot = t2.x + t2.y;
-        for (int off = G / 2; off >= 1; off >>= 1) {
-          sum += __shfl_xor_sync(kFull, sum, off);
-          dot += __shfl_xor_sync(kFull, dot, off);
-        }
-        const float sc = inv_rms<PRECISE>(p, sum);
+        sum_lanes(G, sum, dot);
+        const float sc = live ? inv_rms(p, sum) : 0.f;  // with an eps of 0, 1 / sqrt(0) of a row that is none
         const float2 k2 = splat(-sc * sc * sc * dot * p.inv_D), sc2 = splat(sc);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -360,10 +394,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
           g2[j] = fma2(v2[j], k2, mul2(gw2[j], sc2));
         }
       }
-      if (out.p && on && live) {
-        const int64_t at = now.at(out);
-        store_runs<INTER>(out.p, out.bf16, at + o1, at + o2, g1, g2);
-      }
+      if (out.p && on && live) store_runs<INTER>(out.p, out.bf16, to.at, to.at + gap, g1, g2);
     } else {
       if (p.norm) {
         float2 s2 = splat(0.f);
@@ -373,8 +404,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
           s2 = fma2(v2[j], v2[j], s2);
         }
         float sum = s2.x + s2.y;
-        for (int off = G / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-        const float2 sc2 = splat(inv_rms<PRECISE>(p, sum));
+        sum_lanes(G, sum);
+        const float2 sc2 = splat(inv_rms(p, sum));
         float2 w[4];
         weights(0, w);
 #pragma unroll
@@ -389,13 +420,10 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
         v1[j] = fma2(y, neg2(s[j]), mul2(x, c[j]));
         v2[j] = fma2(x, s[j], mul2(y, c[j]));
       }
-      if (on && live) {
-        const int64_t at = now.at(out);
-        store_runs<INTER>(out.p, out.bf16, at + o1, at + o2, v1, v2);
-      }
+      if (on && live) store_runs<INTER>(out.p, out.bf16, to.at, to.at + gap, v1, v2);
     }
     stage = stage == S - 1 ? 0 : stage + 1;
-    fresh = now.advance(dt, dh, H, L);
+    fresh = advance(now, dt, dh, H, L, to);
   }
   if (!BWD || !p.dw[side]) return;
   // the block's share of dw: the groups' in their order
@@ -440,10 +468,10 @@ __global__ void __launch_bounds__(kThr) qk_pairs_fwd_kernel(const __grid_constan
     load_unit(in.p, PRECISE ? 0 : 1, at, unit_of(p, sub + n * G), live, p.D, v[n]);
     sum = fmaf(v[n][0], v[n][0], fmaf(v[n][1], v[n][1], sum));
   }
-  const double pos = live && p.rot ? position(p, b, t) : 0.0;
+  const double pos = live && p.rot ? position(p, token, t) : 0.0;
   if (p.norm) {
-    for (int off = G / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    sum = inv_rms<PRECISE>(p, sum);
+    sum_lanes(G, sum);
+    sum = inv_rms(p, sum);
   }
 #pragma unroll
   for (int n = 0; n < NU; n++) {
@@ -497,7 +525,7 @@ __global__ void __launch_bounds__(kThr) qk_pairs_bwd_kernel(const __grid_constan
       load_unit(dout.p, dout.bf16, gat, u, live, p.D, g[n]);
       if (p.norm) load_unit(in.p, PRECISE ? 0 : 1, at, u, live, p.D, v[n]);
     }
-    const double pos = p.rot ? position(p, b, t) : 0.0;
+    const double pos = p.rot ? position(p, token, t) : 0.0;
 #pragma unroll
     for (int n = 0; n < NU; n++) {
       if (unit_of(p, sub + n * G).rot) {
@@ -513,11 +541,8 @@ __global__ void __launch_bounds__(kThr) qk_pairs_bwd_kernel(const __grid_constan
       }
     }
     if (p.norm) {
-      for (int off = G / 2; off >= 1; off >>= 1) {
-        sum += __shfl_xor_sync(kFull, sum, off);
-        dot += __shfl_xor_sync(kFull, dot, off);
-      }
-      const float sc = inv_rms<PRECISE>(p, sum), back = sc * sc * dot * p.inv_D;
+      sum_lanes(G, sum, dot);
+      const float sc = inv_rms(p, sum), back = sc * sc * dot * p.inv_D;
 #pragma unroll
       for (int n = 0; n < NU; n++)
 #pragma unroll
@@ -627,7 +652,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
           for (int e = 0; e < TV; e++)
             if (e < m) {
               float cs, sn;
-              turn<PRECISE>(position(p, b, t0 + e), f, p.rot_scale, cs, sn);
+              turn<PRECISE>(position(p, b * p.L + t0 + e, t0 + e), f, p.rot_scale, cs, sn);
               const float x = ga[e], y = gc[e];
               ga[e] = x * cs + y * sn;
               gc[e] = y * cs - x * sn;
@@ -666,7 +691,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
           s += sh[(y * TX + tx) * TV + e];
           if (BWD) q += sh[kThr * TV + (y * TX + tx) * TV + e];
         }
-        sum[e] = inv_rms<PRECISE>(p, s);
+        sum[e] = inv_rms(p, s);
         dot[e] = sum[e] * sum[e] * q * p.inv_D;
       }
     }
@@ -699,7 +724,7 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
             if (p.norm) a[e] *= sum[e] * wa, c[e] *= sum[e] * wc;
             if (u.rot && e < m) {
               float cs, sn;
-              turn<PRECISE>(position(p, b, t0 + e), f, p.rot_scale, cs, sn);
+              turn<PRECISE>(position(p, b * p.L + t0 + e, t0 + e), f, p.rot_scale, cs, sn);
               const float x = a[e], y = c[e];
               a[e] = x * cs - y * sn;
               c[e] = y * cs + x * sn;
@@ -733,21 +758,28 @@ __global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ Q
   }
 }
 
-// dw of both sides from the blocks' shares, in a fixed order: a CTA takes 32 elements of one side,
-// its 8 rows every eighth share each.
-__global__ void __launch_bounds__(256) qk_dw_kernel(const __grid_constant__ QkParams p, int nb0, int nb) {
-  __shared__ float red[8][32];
+// dw of both sides from the blocks' shares, in a fixed order: a CTA takes 32 elements of one side, each of
+// its 32 rows every 32nd share, up to 14 loads in flight.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const __grid_constant__ QkParams p, int nb0, int nb) {
+  __shared__ float red[32][33];
   const int side = blockIdx.y, x = threadIdx.x & 31, y = threadIdx.x >> 5;
   if (!p.dw[side]) return;
   const int j = blockIdx.x * 32 + x, lo = side ? nb0 : 0, hi = side ? nb : nb0;
-  float s = 0.f;
-  if (j < p.D)
-    for (int k = lo + y; k < hi; k += 8) s += p.part[(int64_t)k * p.D + j];
+  float v[kBwdCtas / 32 + 1], s = 0.f;
+#pragma unroll
+  for (int k = 0; k < kBwdCtas / 32 + 1; k++) {
+    const int at = lo + y + 32 * k;
+    v[k] = j < p.D && at < hi ? p.part[(int64_t)at * p.D + j] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kBwdCtas / 32 + 1; k++) s += v[k];
   red[y][x] = s;
   __syncthreads();
-  if (y || j >= p.D) return;
-  for (int k = 1; k < 8; k++) s += red[k][x];
-  p.dw[side][j] = s;
+  s = red[x][y];  // element y's shares
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+  const int e = blockIdx.x * 32 + y;
+  if (x == 0 && e < p.D) p.dw[side][e] = s;
 }
 
 // ---- launchers ---------------------------------------------------------------------------------
@@ -899,7 +931,7 @@ template <typename T> cudaError_t bwd_t(const QkParams &p, cudaStream_t s) {
     e = p.dout[p.H[0] == 0].bf16 ? bwd_rows<T, __nv_bfloat16>(p, &nb0, &nb, s) : bwd_rows<T, float>(p, &nb0, &nb, s);
   }
   if (e != cudaSuccess || (!p.dw[0] && !p.dw[1])) return e;
-  qk_dw_kernel<<<dim3((unsigned)((p.D + 31) / 32), 2), 256, 0, s>>>(p, nb0, nb);
+  qk_dw_kernel<<<dim3((unsigned)((p.D + 31) / 32), 2), 1024, 0, s>>>(p, nb0, nb);
   return cudaGetLastError();
 }
 
