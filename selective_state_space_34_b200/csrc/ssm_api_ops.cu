@@ -198,9 +198,9 @@ ssm::QkParams qk_params(const ssm_qk_args *a) {
 }
 
 // 16-byte accesses: every tensor of a side with heads starts on a 16-byte boundary and steps by multiples of 8
-// elements; with head elements innermost the units of 16 must also tile the rotated part and the rest.
+// elements; with head elements innermost the units of 16 must also tile the head, and of the half layout the rotated part.
 bool qk_vec_ok(const ssm::QkParams &p) {
-  if (!p.time_last && (p.D % 16 != 0 || p.rot % 16 != 0)) return false;
+  if (!p.time_last && (p.D % 16 != 0 || (!p.interleaved && p.rot % 16 != 0))) return false;
   const int64_t rows = p.time_last ? p.D : p.L;
   for (int s = 0; s < 2; s++) {
     if (p.H[s] == 0) continue;

@@ -15,9 +15,8 @@
 // no exchange between lanes. G lanes hold a row (G = units rounded up to a power of two) and add
 // its squares by shuffles. Head sizes, strides or alignments that do not fit take units of one pair.
 //
-// Time innermost (time_last): a thread owns consecutive steps (8 where rows are whole 16-byte runs, else 1)
-// of a few pairs; the squares meet in shared memory, and with more than one pair a thread the elements are
-// read a second time, from L1.
+// Time innermost (time_last): a thread owns consecutive steps of a pair and walks the heads with one set of cosines and
+// sines; the squares of a step meet in shared memory.
 //
 // Angles. In 32 bits position * inv_freq loses the angle of a far position (at 10^6 the spacing is 1/16 of
 // a radian), so the product and its reduction to a fraction of a turn are in 64 bits; what is left
@@ -107,20 +106,6 @@ __device__ __forceinline__ Unit unit_of(const QkParams &p, int u) {
   r.o2 = half ? ur + u : r.o1 + 1;
   return r;
 }
-__device__ __forceinline__ void load_unit(const void *p, int bf16, int64_t at, const Unit &u, bool on, int D, float *v) {
-  v[0] = u.on && on ? ld1(p, bf16, at + u.o1) : 0.f;
-  v[1] = u.on && on && u.o2 < D ? ld1(p, bf16, at + u.o2) : 0.f;
-}
-__device__ __forceinline__ void store_unit(void *p, int bf16, int64_t at, const Unit &u, bool on, int D, const float *v) {
-  if (!u.on || !on) return;
-  st1(p, bf16, at + u.o1, v[0]);
-  if (u.o2 < D) st1(p, bf16, at + u.o2, v[1]);
-}
-__device__ __forceinline__ void load_weights(const float *w, const Unit &u, int D, float *v) {
-  v[0] = w && u.on ? w[u.o1] : 1.f;
-  v[1] = w && u.on && u.o2 < D ? w[u.o2] : 1.f;
-}
-
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
@@ -241,8 +226,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   const int64_t total = p.Bt * p.L * H;
   const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
   const int dt = step / H, dh = step % H;
-  // the lane's unit
-  const int ur = p.rot / 16;
+  // the lane's unit; the interleaved layout may turn some of a unit's pairs
+  const int ur = INTER ? (p.rot + 15) / 16 : p.rot / 16, turned = p.rot / 2 - 8 * sub;
   const bool on = sub < p.D / 16, rot = sub < ur;
   const bool half = rot && !INTER;
   const int o1 = half ? 8 * sub : 16 * sub, o2 = half ? p.rot / 2 + 8 * sub : o1 + 8;
@@ -345,8 +330,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
       const double pos = position(p, now.token, now.t);
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
-        turn<PRECISE>(pos, sf[2 * j + 1][sub], p.rot_scale, c[j].y, s[j].y);
+        if (!INTER || 2 * j < turned) turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
+        if (!INTER || 2 * j + 1 < turned) turn<PRECISE>(pos, sf[2 * j + 1][sub], p.rot_scale, c[j].y, s[j].y);
       }
     }
     cp_async_wait<S - 1>();
@@ -448,328 +433,383 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   }
 }
 
-// Any head size, stride and alignment: units of one pair, NU a lane. G lanes take a row at a time.
-template <typename T, int NU>
-__global__ void __launch_bounds__(kThr) qk_pairs_fwd_kernel(const __grid_constant__ QkParams p, int G) {
+// Any head size, stride and alignment: units of one pair, NU a lane, over the same walk; the next row's elements are
+// loaded into registers while a row is worked on.
+template <typename T, typename Td, bool BWD, int NU>
+__global__ void __launch_bounds__(kThr)
+qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0, int64_t per1) {
   constexpr bool PRECISE = sizeof(T) == 4;
-  const int lane = threadIdx.x & 31, sub = lane & (G - 1);
-  const int64_t heads = p.H[0] + p.H[1], item = ((int64_t)blockIdx.x * kThr + threadIdx.x) / G;
-  int64_t token, h, b, t;
-  divide(item, heads, token, h);
-  divide(token, p.L, b, t);
-  const bool live = b < p.Bt;  // dead groups follow along for the shuffles
-  const int side = h >= p.H[0];
-  if (side) h -= p.H[0];
-  const QkTensor &in = p.in[side], &out = p.out[side];
-  const int64_t at = b * in.sb + t * in.sr + h * in.sh, to = b * out.sb + t * out.sr + h * out.sh;
-  float v[NU][2], sum = 0.f;
-#pragma unroll
-  for (int n = 0; n < NU; n++) {
-    load_unit(in.p, PRECISE ? 0 : 1, at, unit_of(p, sub + n * G), live, p.D, v[n]);
-    sum = fmaf(v[n][0], v[n][0], fmaf(v[n][1], v[n][1], sum));
-  }
-  const double pos = live && p.rot ? position(p, token, t) : 0.0;
-  if (p.norm) {
-    sum_lanes(G, sum);
-    sum = inv_rms(p, sum);
-  }
+  extern __shared__ float sdw[];  // (groups, D) sums of dw
+  const int side = (int)blockIdx.x >= nb0;
+  const int block = side ? blockIdx.x - nb0 : blockIdx.x;
+  const int lane = threadIdx.x & 31, sub = lane & (G - 1), grp = lane / G, step = 32 / G;
+  const int64_t per = side ? per1 : per0;
+  const int H = p.H[side], L = (int)p.L;
+  const QkTensor in = p.in[side], dout = p.dout[side], out = p.out[side];
+  const int64_t first = ((int64_t)block * (kThr / 32) + (threadIdx.x >> 5)) * per;
+  const int64_t total = p.Bt * p.L * H;
+  const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
+  const int dt = step / H, dh = step % H;
+  const bool reads_v = !BWD || p.norm;
+  // the lane's units: first element, distance to the second (0: none), weights, sums of dw
+  int o[NU], gap[NU];
+  bool on[NU], rot[NU];
+  float w[NU][2], dw[NU][2], c[NU], s[NU];
 #pragma unroll
   for (int n = 0; n < NU; n++) {
     const Unit u = unit_of(p, sub + n * G);
-    if (p.norm) {
-      float w[2];
-      load_weights(p.w[side], u, p.D, w);
-      v[n][0] *= sum * w[0];
-      v[n][1] *= sum * w[1];
+    on[n] = u.on;
+    rot[n] = u.on && u.rot;
+    o[n] = u.o1;
+    gap[n] = u.o2 < p.D ? u.o2 - u.o1 : 0;
+    w[n][0] = w[n][1] = c[n] = 1.f;
+    dw[n][0] = dw[n][1] = s[n] = 0.f;
+    if (p.norm && p.w[side] && u.on) {
+      w[n][0] = p.w[side][u.o1];
+      if (gap[n]) w[n][1] = p.w[side][u.o2];
     }
-    if (u.rot) {
-      float c, s;
-      turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c, s);
-      const float x = v[n][0], y = v[n][1];
-      v[n][0] = x * c - y * s;
-      v[n][1] = y * c + x * s;
-    }
-    store_unit(out.p, out.bf16, to, u, live, p.D, v[n]);
   }
-}
-
-// Groups of lanes walk the rows of one side (blocks [0, nb0) the queries, the others the keys) with a stride
-// of the side's groups and keep their share of dw in registers.
-template <typename T, int NU>
-__global__ void __launch_bounds__(kThr) qk_pairs_bwd_kernel(const __grid_constant__ QkParams p, int G, int nb0) {
-  constexpr bool PRECISE = sizeof(T) == 4;
-  extern __shared__ float sdw[];  // (groups, D) with dw
-  const int side = (int)blockIdx.x >= nb0;
-  const int64_t block = side ? blockIdx.x - nb0 : blockIdx.x, blocks = side ? gridDim.x - nb0 : nb0;
-  const int lane = threadIdx.x & 31, sub = lane & (G - 1), per_cta = kThr / G;
-  const int64_t items = p.Bt * p.L * p.H[side];
-  const QkTensor in = p.in[side], dout = p.dout[side], out = p.out[side];
-  float w[NU][2], dw[NU][2];
-#pragma unroll
-  for (int n = 0; n < NU; n++) {
-    if (p.norm) load_weights(p.w[side], unit_of(p, sub + n * G), p.D, w[n]);
-    dw[n][0] = dw[n][1] = 0.f;
-  }
-  // the trip count is the block's, so that every lane of a warp is there for the shuffles
-  for (int64_t i0 = block * per_cta; i0 < items; i0 += blocks * per_cta) {
-    const int64_t item = i0 + threadIdx.x / G;
-    const bool live = item < items;
-    int64_t token, h, b, t;
-    divide(live ? item : 0, p.H[side], token, h);
-    divide(token, p.L, b, t);
-    float v[NU][2], g[NU][2], sum = 0.f, dot = 0.f;
-    const int64_t gat = b * dout.sb + t * dout.sr + h * dout.sh, at = b * in.sb + t * in.sr + h * in.sh;
+  Walk ahead, now;
+  int64_t b0;
+  ahead.start(first + grp, H, L, b0);
+  now = ahead;
+  Place from(in, ahead, b0, dt, dh, H, L, 0), dfrom(dout, ahead, b0, dt, dh, H, L, 0), to(out, now, b0, dt, dh, H, L, 0);
+  T nv[NU][2];
+  Td ng[NU][2];
+  int left = n_rows - grp;
+  auto fetch = [&]() {
+    const T *a = static_cast<const T *>(in.p) + from.at;
+    const Td *g = static_cast<const Td *>(dout.p) + dfrom.at;
 #pragma unroll
     for (int n = 0; n < NU; n++) {
-      const Unit u = unit_of(p, sub + n * G);
-      load_unit(dout.p, dout.bf16, gat, u, live, p.D, g[n]);
-      if (p.norm) load_unit(in.p, PRECISE ? 0 : 1, at, u, live, p.D, v[n]);
+      nv[n][0] = nv[n][1] = from_f32<T>(0.f);
+      ng[n][0] = ng[n][1] = from_f32<Td>(0.f);
+      if (left > 0 && on[n]) {
+        if (reads_v) {
+          nv[n][0] = a[o[n]];
+          if (gap[n]) nv[n][1] = a[o[n] + gap[n]];
+        }
+        if (BWD) {
+          ng[n][0] = g[o[n]];
+          if (gap[n]) ng[n][1] = g[o[n] + gap[n]];
+        }
+      }
     }
-    const double pos = p.rot ? position(p, token, t) : 0.0;
+    left -= step;
+    if (BWD) advance(ahead, dt, dh, H, L, from, dfrom);
+    else advance(ahead, dt, dh, H, L, from);
+  };
+  fetch();
+  bool fresh = true;
+  for (int i = 0; i < n_rows; i += step) {
+    const bool live = i + grp < n_rows;
+    float v[NU][2], g[NU][2];
 #pragma unroll
-    for (int n = 0; n < NU; n++) {
-      if (unit_of(p, sub + n * G).rot) {
-        float c, s;
-        turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c, s);
-        const float x = g[n][0], y = g[n][1];
-        g[n][0] = x * c + y * s;
-        g[n][1] = y * c - x * s;
+    for (int n = 0; n < NU; n++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        v[n][e] = to_f32(nv[n][e]);
+        if (BWD) g[n][e] = to_f32(ng[n][e]);
       }
-      if (p.norm) {
-        sum = fmaf(v[n][0], v[n][0], fmaf(v[n][1], v[n][1], sum));
-        dot = fmaf(g[n][0] * w[n][0], v[n][0], fmaf(g[n][1] * w[n][1], v[n][1], dot));
-      }
-    }
-    if (p.norm) {
-      sum_lanes(G, sum, dot);
-      const float sc = inv_rms(p, sum), back = sc * sc * dot * p.inv_D;
+    fetch();
+    if (fresh && live && p.rot) {
+      const double pos = position(p, now.token, now.t);
 #pragma unroll
       for (int n = 0; n < NU; n++)
+        if (rot[n]) turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c[n], s[n]);
+    }
+    float sum = 0.f, dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-          dw[n][e] = fmaf(g[n][e] * sc, v[n][e], dw[n][e]);
-          g[n][e] = sc * (g[n][e] * w[n][e] - v[n][e] * back);
+    for (int n = 0; n < NU; n++) {
+      if (BWD) {
+        const float x = g[n][0], y = g[n][1];
+        g[n][0] = x * c[n] + y * s[n];
+        g[n][1] = y * c[n] - x * s[n];
+        dot = fmaf(g[n][0] * w[n][0], v[n][0], fmaf(g[n][1] * w[n][1], v[n][1], dot));
+      }
+      sum = fmaf(v[n][0], v[n][0], fmaf(v[n][1], v[n][1], sum));
+    }
+    float sc = 1.f, back = 0.f;
+    if (p.norm) {
+      sum_lanes(G, sum, dot);
+      sc = live ? inv_rms(p, sum) : 0.f;  // with an eps of 0, 1 / sqrt(0) of a row that is none
+      back = sc * sc * dot * p.inv_D;
+    }
+#pragma unroll
+    for (int n = 0; n < NU; n++) {
+      float x, y;
+      if (BWD) {
+        if (p.norm) {
+          dw[n][0] = fmaf(g[n][0] * sc, v[n][0], dw[n][0]);
+          dw[n][1] = fmaf(g[n][1] * sc, v[n][1], dw[n][1]);
         }
+        x = p.norm ? sc * (g[n][0] * w[n][0] - v[n][0] * back) : g[n][0];
+        y = p.norm ? sc * (g[n][1] * w[n][1] - v[n][1] * back) : g[n][1];
+      } else {
+        const float a = v[n][0] * (sc * w[n][0]), b = v[n][1] * (sc * w[n][1]);
+        x = a * c[n] - b * s[n];
+        y = b * c[n] + a * s[n];
+      }
+      if (out.p && live && on[n]) {
+        st1(out.p, out.bf16, to.at + o[n], x);
+        if (gap[n]) st1(out.p, out.bf16, to.at + o[n] + gap[n], y);
+      }
     }
-    if (out.p) {
-      const int64_t to = b * out.sb + t * out.sr + h * out.sh;
-#pragma unroll
-      for (int n = 0; n < NU; n++) store_unit(out.p, out.bf16, to, unit_of(p, sub + n * G), live, p.D, g[n]);
-    }
+    fresh = advance(now, dt, dh, H, L, to);
   }
-  if (!p.dw[side]) return;
+  if (!BWD || !p.dw[side]) return;
   // the block's share of dw: the groups' in their order
 #pragma unroll
-  for (int n = 0; n < NU; n++) {
-    const Unit u = unit_of(p, sub + n * G);
-    if (!u.on) continue;
-    float *row = sdw + (threadIdx.x / G) * p.D;
-    row[u.o1] = dw[n][0];
-    if (u.o2 < p.D) row[u.o2] = dw[n][1];
-  }
+  for (int n = 0; n < NU; n++)
+    if (on[n]) {
+      float *row = sdw + (threadIdx.x / G) * p.D + o[n];
+      row[0] = dw[n][0];
+      if (gap[n]) row[gap[n]] = dw[n][1];
+    }
   __syncthreads();
   for (int j = threadIdx.x; j < p.D; j += kThr) {
-    float s = 0.f;
-    for (int r = 0; r < per_cta; r++) s += sdw[r * p.D + j];
-    p.part[(int64_t)blockIdx.x * p.D + j] = s;
+    float t = 0.f;
+    for (int r = 0; r < kThr / G; r++) t += sdw[r * p.D + j];
+    p.part[(int64_t)blockIdx.x * p.D + j] = t;
   }
 }
 
 // ---- time innermost ----------------------------------------------------------------------------
 
-// TX threads over time, TV steps each, TY = kThr / TX over the pairs of a head, NS pairs a thread.
-// A pair unit is unit_of: elements o1 and o2 (or o1 alone at an odd end).
-template <typename T, int TV> struct TimeLoad {
-  static __device__ __forceinline__ void get(const void *p, int bf16, int64_t i, int n, float *v) {
-    if constexpr (TV == 8) {
-      if (n == 8) {
-        ld8any(p, bf16, i, v);
-        return;
-      }
+// m of the TV consecutive elements at i.
+template <int TV> __device__ __forceinline__ void get_run(const void *p, int bf16, int64_t i, int m, float *v) {
+  if constexpr (TV == 8) {
+    if (m == 8) {
+      ld8any(p, bf16, i, v);
+      return;
     }
-#pragma unroll
-    for (int e = 0; e < TV; e++) v[e] = e < n ? ld1(p, bf16, i + e) : 0.f;
   }
-  static __device__ __forceinline__ void put(void *p, int bf16, int64_t i, int n, const float *v) {
-    if constexpr (TV == 8) {
-      if (n == 8) {
-        st8any(p, bf16, i, v);
-        return;
-      }
+#pragma unroll
+  for (int e = 0; e < TV; e++) v[e] = e < m ? ld1(p, bf16, i + e) : 0.f;
+}
+template <int TV> __device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, const float *v) {
+  if constexpr (TV == 8) {
+    if (m == 8) {
+      st8any(p, bf16, i, v);
+      return;
     }
-#pragma unroll
-    for (int e = 0; e < TV; e++)
-      if (e < n) st1(p, bf16, i + e, v[e]);
   }
-};
+#pragma unroll
+  for (int e = 0; e < TV; e++)
+    if (e < m) st1(p, bf16, i + e, v[e]);
+}
 
-// A tile: (batch, head, kThr / TY * TV steps). Forward: one per CTA. Backward: the CTAs of a side walk
-// its tiles and keep dw in registers.
+// A tile is TX * TV steps of one batch element and a chunk of its heads (queries, then keys). A thread owns TV
+// consecutive steps (8 where rows are whole 16-byte runs, else 1) of NS pairs, every TY-th, TY = kThr / TX; a
+// pair unit is elements o1 and o2 (or o1 alone at an odd end). The squares of a step meet in shared memory. With one
+// pair a thread the elements stay in registers and its cosines and sines serve every head of the chunk; with more
+// the elements are read a second time, from L1.
 template <typename T, int TV, int NS, bool BWD>
-__global__ void __launch_bounds__(kThr) qk_time_kernel(const __grid_constant__ QkParams p, int TX, int nb0, int64_t tiles0, int64_t tiles1) {
+__global__ void __launch_bounds__(kThr)
+qk_time_kernel(const __grid_constant__ QkParams p, int TX, int heads, int64_t chunks, int64_t tiles) {
   constexpr bool PRECISE = sizeof(T) == 4;
-  using M = TimeLoad<T, TV>;
-  extern __shared__ float sh[];  // sums over the pairs: (TY, TX * TV), twice for the backward
+  extern __shared__ __align__(16) float sh[];
   const int TY = kThr / TX, tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-  const int side = BWD ? (int)blockIdx.x >= nb0 : 0;
-  const int64_t span = (int64_t)TX * TV, per_row = (p.L + span - 1) / span;
-  const int64_t tiles = BWD ? (side ? tiles1 : tiles0) : tiles0 + tiles1;
-  const int64_t first = BWD && side ? blockIdx.x - nb0 : blockIdx.x;
-  const int64_t stride = !BWD ? gridDim.x : side ? gridDim.x - nb0 : nb0;
-  const int n_units = p.rot / 2 + (p.D - p.rot + 1) / 2;
-  float dwa[NS], dwb[NS];
+  const int span = TX * TV, per_row = (int)((p.L + span - 1) / span);
+  // R threads add the squares of one step; rows of sh are padded so that they hit different banks
+  const int R = span < kThr ? kThr / span : 1, pitch = span + 32 / R;
+  float *const sums = sh, *const dots = sh + TY * pitch, *const res = sh + (BWD ? 2 : 1) * TY * pitch, *const res2 = res + span;
+  const int n_units = p.rot / 2 + (p.D - p.rot + 1) / 2, all = p.H[0] + p.H[1];
+  float dw[2][NS][2];
 #pragma unroll
-  for (int n = 0; n < NS; n++) dwa[n] = dwb[n] = 0.f;
-  for (int64_t tile = first; tile < tiles; tile += stride) {
-    const int sd = BWD ? side : tile >= tiles0;
-    const QkTensor &in = p.in[sd], &out = p.out[sd];
-    int64_t bh, tt, b, h;
-    divide(!BWD && sd ? tile - tiles0 : tile, per_row, bh, tt);
-    divide(bh, p.H[sd], b, h);
+  for (int n = 0; n < NS; n++) dw[0][n][0] = dw[0][n][1] = dw[1][n][0] = dw[1][n][1] = 0.f;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    int64_t bc, tt, b, chunk;
+    divide(tile, per_row, bc, tt);
+    divide(bc, chunks, b, chunk);
     const int64_t t0 = tt * span + (int64_t)tx * TV;
     const int m = (int)(p.L - t0 < 0 ? 0 : p.L - t0 < TV ? p.L - t0 : TV);  // live steps of this thread
-    const int64_t at = b * in.sb + h * in.sh + t0;
-    const int64_t dat = BWD ? b * p.dout[sd].sb + h * p.dout[sd].sh + t0 : 0;
-    const int64_t oat = b * out.sb + h * out.sh + t0;
-    float a[TV], c[TV], ga[TV], gc[TV];  // the elements of a pair, and their gradients
-    float sum[TV], dot[TV];
+    float cs[TV], sn[TV];
+    auto angles = [&](const Unit &u, int unit) {
+      const double f = u.rot ? frequency(p, unit) : 0.0;
 #pragma unroll
-    for (int e = 0; e < TV; e++) sum[e] = dot[e] = 0.f;
-    // the elements of pair unit u, its gradients turned back
-    auto fetch = [&](const Unit &u, int unit) {
-      const bool two = u.o2 < p.D;
-      if (!BWD || p.norm) {
-        M::get(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m, a);
-        M::get(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, two ? m : 0, c);
-      }
-      if (BWD) {
-        const QkTensor &dt = p.dout[sd];
-        M::get(dt.p, dt.bf16, dat + u.o1 * dt.sr, m, ga);
-        M::get(dt.p, dt.bf16, dat + u.o2 * dt.sr, two ? m : 0, gc);
-        if (u.rot) {
-          const double f = frequency(p, unit);
-#pragma unroll
-          for (int e = 0; e < TV; e++)
-            if (e < m) {
-              float cs, sn;
-              turn<PRECISE>(position(p, b * p.L + t0 + e, t0 + e), f, p.rot_scale, cs, sn);
-              const float x = ga[e], y = gc[e];
-              ga[e] = x * cs + y * sn;
-              gc[e] = y * cs - x * sn;
-            }
-        }
+      for (int e = 0; e < TV; e++) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+        if (u.rot && e < m) turn<PRECISE>(position(p, b * p.L + t0 + e, t0 + e), f, p.rot_scale, cs[e], sn[e]);
       }
     };
-    auto weight = [&](int o) { return p.w[sd] ? p.w[sd][o] : 1.f; };
-    if (p.norm) {
+    if (NS == 1) angles(unit_of(p, ty), ty);
+    const int h_end = min(all, (int)(chunk + 1) * heads);
+    for (int hh = (int)chunk * heads; hh < h_end; hh++) {
+      const int sd = hh >= p.H[0], h = sd ? hh - p.H[0] : hh;
+      const QkTensor &in = p.in[sd], &out = p.out[sd], &dout = p.dout[sd];
+      const int64_t at = b * in.sb + h * in.sh + t0, dat = BWD ? b * dout.sb + h * dout.sh + t0 : 0;
+      const int64_t oat = b * out.sb + h * out.sh + t0;
+      float a[TV], c[TV], ga[TV], gc[TV];  // the elements of a pair, and their gradients turned back
+      auto fetch = [&](const Unit &u, int unit) {
+        const int m2 = u.o2 < p.D ? m : 0;
+        if (!BWD || p.norm) {
+          get_run<TV>(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m, a);
+          get_run<TV>(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, m2, c);
+        }
+        if (BWD) {
+          get_run<TV>(dout.p, dout.bf16, dat + u.o1 * dout.sr, m, ga);
+          get_run<TV>(dout.p, dout.bf16, dat + u.o2 * dout.sr, m2, gc);
+          if (NS > 1) angles(u, unit);
+#pragma unroll
+          for (int e = 0; e < TV; e++) {
+            const float x = ga[e], y = gc[e];
+            ga[e] = x * cs[e] + y * sn[e];
+            gc[e] = y * cs[e] - x * sn[e];
+          }
+        }
+      };
+      const float *w = p.w[sd];
+      float sc[TV], back[TV];
+#pragma unroll
+      for (int e = 0; e < TV; e++) sc[e] = back[e] = 0.f;
+      if (p.norm) {
+#pragma unroll
+        for (int n = 0; n < NS; n++) {
+          const int unit = ty + n * TY;
+          if (unit < n_units) {
+            const Unit u = unit_of(p, unit);
+            fetch(u, unit);
+            const float wa = BWD ? (w ? w[u.o1] : 1.f) : 0.f, wc = BWD && u.o2 < p.D ? (w ? w[u.o2] : 1.f) : 0.f;
+#pragma unroll
+            for (int e = 0; e < TV; e++) {
+              sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
+              if (BWD) back[e] = fmaf(ga[e] * wa, a[e], fmaf(gc[e] * wc, c[e], back[e]));
+            }
+          }
+        }
+        // every thread's partial sums, then a step's over its TY threads in a fixed order
+        if constexpr (TV == 8) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4 *>(sums + ty * pitch + tx * 8 + e) = make_float4(sc[e], sc[e + 1], sc[e + 2], sc[e + 3]);
+            if (BWD)
+              *reinterpret_cast<float4 *>(dots + ty * pitch + tx * 8 + e) = make_float4(back[e], back[e + 1], back[e + 2], back[e + 3]);
+          }
+        } else {
+          sums[ty * pitch + tx] = sc[0];
+          if (BWD) dots[ty * pitch + tx] = back[0];
+        }
+        __syncthreads();
+        for (int k = threadIdx.x / R; k < span; k += kThr / R) {
+          float s = 0.f, d = 0.f;
+          for (int y = threadIdx.x % R; y < TY; y += R) {
+            s += sums[y * pitch + k];
+            if (BWD) d += dots[y * pitch + k];
+          }
+          for (int off = R / 2; off >= 1; off >>= 1) {
+            s += __shfl_xor_sync(kFull, s, off);
+            if (BWD) d += __shfl_xor_sync(kFull, d, off);
+          }
+          if (threadIdx.x % R == 0) {
+            const float r = inv_rms(p, s);
+            res[k] = r;
+            if (BWD) res2[k] = r * r * d * p.inv_D;
+          }
+        }
+        __syncthreads();  // the sums are read; the next head's go in after the next barrier of this kind
+#pragma unroll
+        for (int e = 0; e < TV; e++) {
+          sc[e] = res[tx * TV + e];
+          if (BWD) back[e] = res2[tx * TV + e];
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NS; n++) {
         const int unit = ty + n * TY;
         if (unit < n_units) {
           const Unit u = unit_of(p, unit);
-          fetch(u, unit);
-          const float wa = BWD ? weight(u.o1) : 0.f, wc = BWD && u.o2 < p.D ? weight(u.o2) : 0.f;
+          const bool two = u.o2 < p.D;
+          if (NS > 1 || !p.norm) fetch(u, unit);  // with one pair it is still here
+          const float wa = w ? w[u.o1] : 1.f, wc = w && two ? w[u.o2] : 1.f;
+          if (BWD) {
+            if (p.norm) {
+              float x = 0.f, y = 0.f;
 #pragma unroll
-          for (int e = 0; e < TV; e++) {
-            sum[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sum[e]));
-            if (BWD) dot[e] = fmaf(ga[e] * wa, a[e], fmaf(gc[e] * wc, c[e], dot[e]));
-          }
-        }
-      }
-      // over the threads that share a step, in their order
-      __syncthreads();  // the tile before has been read
-#pragma unroll
-      for (int e = 0; e < TV; e++) {
-        sh[(ty * TX + tx) * TV + e] = sum[e];
-        if (BWD) sh[kThr * TV + (ty * TX + tx) * TV + e] = dot[e];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < TV; e++) {
-        float s = 0.f, q = 0.f;
-        for (int y = 0; y < TY; y++) {
-          s += sh[(y * TX + tx) * TV + e];
-          if (BWD) q += sh[kThr * TV + (y * TX + tx) * TV + e];
-        }
-        sum[e] = inv_rms(p, s);
-        dot[e] = sum[e] * sum[e] * q * p.inv_D;
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NS; n++) {
-      const int unit = ty + n * TY;
-      if (unit < n_units) {
-        const Unit u = unit_of(p, unit);
-        const bool two = u.o2 < p.D;
-        if (NS > 1 || !p.norm) fetch(u, unit);  // with one pair it is still here
-        const float wa = p.norm ? weight(u.o1) : 1.f, wc = p.norm && two ? weight(u.o2) : 1.f;
-        if (BWD) {
-          if (p.norm) {
+              for (int e = 0; e < TV; e++) {
+                if (e < m) {  // a step that is none has no 1 / sqrt(0) either
+                  x = fmaf(ga[e] * sc[e], a[e], x);
+                  y = fmaf(gc[e] * sc[e], c[e], y);
+                }
+                ga[e] = sc[e] * (ga[e] * wa - a[e] * back[e]);
+                gc[e] = sc[e] * (gc[e] * wc - c[e] * back[e]);
+              }
+              dw[0][n][0] += sd ? 0.f : x;
+              dw[0][n][1] += sd ? 0.f : y;
+              dw[1][n][0] += sd ? x : 0.f;
+              dw[1][n][1] += sd ? y : 0.f;
+            }
+            if (out.p) {
+              put_run<TV>(out.p, out.bf16, oat + u.o1 * out.sr, m, ga);
+              if (two) put_run<TV>(out.p, out.bf16, oat + u.o2 * out.sr, m, gc);
+            }
+          } else {
+            if (NS > 1) angles(u, unit);
 #pragma unroll
             for (int e = 0; e < TV; e++) {
-              dwa[n] = fmaf(ga[e] * sum[e], a[e], dwa[n]);
-              dwb[n] = fmaf(gc[e] * sum[e], c[e], dwb[n]);
-              ga[e] = sum[e] * (ga[e] * wa - a[e] * dot[e]);
-              gc[e] = sum[e] * (gc[e] * wc - c[e] * dot[e]);
+              const float x = p.norm ? a[e] * (sc[e] * wa) : a[e], y = p.norm ? c[e] * (sc[e] * wc) : c[e];
+              a[e] = x * cs[e] - y * sn[e];
+              c[e] = y * cs[e] + x * sn[e];
             }
+            put_run<TV>(out.p, out.bf16, oat + u.o1 * out.sr, m, a);
+            if (two) put_run<TV>(out.p, out.bf16, oat + u.o2 * out.sr, m, c);
           }
-          if (out.p) {
-            M::put(out.p, out.bf16, oat + u.o1 * out.sr, m, ga);
-            if (two) M::put(out.p, out.bf16, oat + u.o2 * out.sr, m, gc);
-          }
-        } else {
-          const double f = u.rot ? frequency(p, unit) : 0.0;
-#pragma unroll
-          for (int e = 0; e < TV; e++) {
-            if (p.norm) a[e] *= sum[e] * wa, c[e] *= sum[e] * wc;
-            if (u.rot && e < m) {
-              float cs, sn;
-              turn<PRECISE>(position(p, b * p.L + t0 + e, t0 + e), f, p.rot_scale, cs, sn);
-              const float x = a[e], y = c[e];
-              a[e] = x * cs - y * sn;
-              c[e] = y * cs + x * sn;
-            }
-          }
-          M::put(out.p, out.bf16, oat + u.o1 * out.sr, m, a);
-          if (two) M::put(out.p, out.bf16, oat + u.o2 * out.sr, m, c);
         }
       }
     }
   }
-  if (!BWD || !p.dw[side]) return;
-  // the block's share of dw: over the TX threads that share a pair, in their order
+  if (!BWD || (!p.dw[0] && !p.dw[1])) return;
+  // the block's shares of dw, rows 2 block + side: over the TX threads of a pair
+  const int lanes = TX < 32 ? TX : 32;
 #pragma unroll
-  for (int n = 0; n < NS; n++) {
-    __syncthreads();
-    sh[2 * threadIdx.x] = dwa[n];
-    sh[2 * threadIdx.x + 1] = dwb[n];
-    __syncthreads();
-    const int unit = ty + n * TY;
-    if (tx == 0 && unit < n_units) {
-      const Unit u = unit_of(p, unit);
-      float x = 0.f, y = 0.f;
-      for (int k = 0; k < TX; k++) {
-        x += sh[2 * (ty * TX + k)];
-        y += sh[2 * (ty * TX + k) + 1];
+  for (int sd = 0; sd < 2; sd++) {
+    if (!p.dw[sd]) continue;
+#pragma unroll
+    for (int n = 0; n < NS; n++) {
+      float x = dw[sd][n][0], y = dw[sd][n][1];
+      for (int off = lanes / 2; off >= 1; off >>= 1) {
+        x += __shfl_xor_sync(kFull, x, off);
+        y += __shfl_xor_sync(kFull, y, off);
       }
-      p.part[(int64_t)blockIdx.x * p.D + u.o1] = x;
-      if (u.o2 < p.D) p.part[(int64_t)blockIdx.x * p.D + u.o2] = y;
+      if (TX > 32) {
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) {
+          sh[threadIdx.x / 16] = x;
+          sh[threadIdx.x / 16 + 1] = y;
+        }
+        __syncthreads();
+        x = y = 0.f;
+        for (int k = 0; k < TX / 32; k++) {
+          x += sh[2 * (ty * (TX / 32) + k)];
+          y += sh[2 * (ty * (TX / 32) + k) + 1];
+        }
+      }
+      const int unit = ty + n * TY;
+      if (tx == 0 && unit < n_units) {
+        const Unit u = unit_of(p, unit);
+        float *row = p.part + (2 * (int64_t)blockIdx.x + sd) * p.D;
+        row[u.o1] = x;
+        if (u.o2 < p.D) row[u.o2] = y;
+      }
     }
   }
 }
 
-// dw of both sides from the blocks' shares, in a fixed order: a CTA takes 32 elements of one side, each of
-// its 32 rows every 32nd share, up to 14 loads in flight.
-__global__ void __launch_bounds__(1024) qk_dw_kernel(const __grid_constant__ QkParams p, int nb0, int nb) {
+// dw of both sides from the blocks' shares, in a fixed order: side 0's are every stride-th of the first nb0 rows, side
+// 1's every stride-th of the others from lo1. A CTA takes 32 elements of one side, each of its 32 rows every 32nd share, all
+// loads in flight.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const __grid_constant__ QkParams p, int n0, int lo1, int n1, int stride) {
   __shared__ float red[32][33];
   const int side = blockIdx.y, x = threadIdx.x & 31, y = threadIdx.x >> 5;
   if (!p.dw[side]) return;
-  const int j = blockIdx.x * 32 + x, lo = side ? nb0 : 0, hi = side ? nb : nb0;
+  const int j = blockIdx.x * 32 + x, n = side ? n1 : n0;
+  const float *part = p.part + (side ? (int64_t)lo1 * p.D : 0);
   float v[kBwdCtas / 32 + 1], s = 0.f;
 #pragma unroll
   for (int k = 0; k < kBwdCtas / 32 + 1; k++) {
-    const int at = lo + y + 32 * k;
-    v[k] = j < p.D && at < hi ? p.part[(int64_t)at * p.D + j] : 0.f;
+    const int at = y + 32 * k;
+    v[k] = j < p.D && at < n ? part[(int64_t)at * stride * p.D + j] : 0.f;
   }
 #pragma unroll
   for (int k = 0; k < kBwdCtas / 32 + 1; k++) s += v[k];
@@ -792,29 +832,35 @@ int pow2_at_least(int n) {
   return g;
 }
 
+// Pair units of a row.
+int pairs_of(const QkParams &p) { return p.rot / 2 + (p.D - p.rot + 1) / 2; }
+
 // Lanes that hold a row: a unit of 16 elements each (vec); at least a fourth of the pairs otherwise, at most a warp.
 int lanes_per_row(const QkParams &p) {
   if (p.vec) return pow2_at_least(p.D / 16);
-  const int pairs = p.rot / 2 + (p.D - p.rot + 1) / 2, g = pow2_at_least((pairs + 3) / 4);
+  const int g = pow2_at_least((pairs_of(p) + 3) / 4);
   return g < 32 ? g : 32;
 }
 
-// Threads over time of a time_last tile: as few pairs a thread as possible, 8 threads over time at least.
-int time_lanes(const QkParams &p) {
-  const int units = p.rot / 2 + (p.D - p.rot + 1) / 2;
-  const int ty = pow2_at_least(units);
-  return kThr / (ty < 32 ? ty : 32);
-}
-
+// Time innermost: threads over time, heads per tile, tiles, shared memory. As few pairs a thread as possible with 8
+// threads (of 8 steps) or 32 (of one step) over time at least, so that a row's accesses are 64 bytes and more; all heads of
+// a batch element in one tile, for their common angles, where that leaves two tiles per SM.
 struct TimePlan {
-  int TX;
-  int64_t tiles[2];
+  int TX, heads;
+  int64_t chunks, tiles;
+  int smem;
 };
-TimePlan time_plan(const QkParams &p) {
+TimePlan time_plan(const QkParams &p, bool bwd) {
   TimePlan t;
-  t.TX = time_lanes(p);
-  const int64_t span = (int64_t)t.TX * (p.vec ? 8 : 1);
-  for (int s = 0; s < 2; s++) t.tiles[s] = p.Bt * p.H[s] * ((p.L + span - 1) / span);
+  const int TV = p.vec ? 8 : 1, ty = pow2_at_least(pairs_of(p)), most = p.vec ? 32 : 8;
+  t.TX = kThr / (ty < most ? ty : most);
+  const int span = t.TX * TV, R = span < kThr ? kThr / span : 1;
+  const int64_t slices = p.Bt * ((p.L + span - 1) / span);
+  const int all = p.H[0] + p.H[1];
+  t.heads = slices >= 2 * 148 ? all : 1;
+  t.chunks = (all + t.heads - 1) / t.heads;
+  t.tiles = slices * t.chunks;
+  t.smem = (int)sizeof(float) * ((bwd ? 2 : 1) * (kThr / t.TX) * (span + 32 / R) + 2 * span);
   return t;
 }
 
@@ -831,116 +877,102 @@ void split_blocks(const int64_t *work, int64_t most, int *nb0, int *nb1) {
   *nb1 = (int)n[1];
 }
 
-template <typename T, typename Td, bool BWD, bool INTER>
-cudaError_t rows_launch(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
+// How the rows of both sides are cut: CTAs of the queries and of both, rows per warp (whole steps of 32 / G rows).
+struct RowPlan {
+  int G, nb0, nb;
+  int64_t per[2];
+};
+bool plan_rows(const QkParams &p, int64_t most, RowPlan *r) {
   constexpr int kWarps = kThr / 32;
-  const int G = lanes_per_row(p), step = 32 / G;
-  int64_t rows[2], work[2], per[2] = {1, 1};
+  r->G = lanes_per_row(p);
+  const int step = 32 / r->G;
+  int64_t rows[2], work[2];
+  int n[2];
   for (int j = 0; j < 2; j++) {
     rows[j] = p.Bt * p.L * p.H[j];
     work[j] = (rows[j] + kWarps * step - 1) / (kWarps * step);
   }
-  int n[2];
-  split_blocks(work, 148 * (BWD ? 2 : 3), &n[0], &n[1]);
-  for (int j = 0; j < 2; j++) {  // rows per warp, whole steps
+  split_blocks(work, most, &n[0], &n[1]);
+  for (int j = 0; j < 2; j++) {
+    r->per[j] = step;
     if (!n[j]) continue;
-    per[j] = (rows[j] + (int64_t)n[j] * kWarps - 1) / ((int64_t)n[j] * kWarps);
-    per[j] = (per[j] + step - 1) / step * step;
-    if (per[j] > 0x7fffff00) return cudaErrorInvalidConfiguration;
+    const int64_t warps = (int64_t)n[j] * kWarps, per = (rows[j] + warps - 1) / warps;
+    r->per[j] = (per + step - 1) / step * step;
+    if (r->per[j] > 0x7fffff00) return false;
   }
-  *nb0 = n[0];
-  *nb = n[0] + n[1];
-  constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
-  const int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>, sums = (int)sizeof(float) * (kThr / G) * p.D;
-  const int smem = BWD && sums > ring ? sums : ring;
-  const auto kernel = qk_rows_kernel<T, Td, BWD, INTER>;
-  if (smem > 47 * 1024) {
+  r->nb0 = n[0];
+  r->nb = n[0] + n[1];
+  return true;
+}
+
+template <typename K> cudaError_t launch_rows(K kernel, const QkParams &p, const RowPlan &r, int smem, cudaStream_t s) {
+  if (smem > 40 * 1024) {  // with the kernels' own 4 KB more than the default 48 KB
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<*nb, kThr, smem, s>>>(p, G, n[0], per[0], per[1]);
+  kernel<<<r.nb, kThr, smem, s>>>(p, r.G, r.nb0, r.per[0], r.per[1]);
   return cudaGetLastError();
 }
 
-template <typename T, int NU> cudaError_t pairs_fwd(const QkParams &p, cudaStream_t s) {
-  const int G = lanes_per_row(p);
-  const int64_t blocks = (p.Bt * p.L * (p.H[0] + p.H[1]) * G + kThr - 1) / kThr;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  qk_pairs_fwd_kernel<T, NU><<<(unsigned)blocks, kThr, 0, s>>>(p, G);
-  return cudaGetLastError();
+// Head elements innermost, forward (Td = T) or backward. CTAs: what fits the SMs at once, at most kBwdCtas of a backward.
+template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams &p, RowPlan *r, cudaStream_t s) {
+  if (!plan_rows(p, BWD ? (p.vec ? 148 * 2 : kBwdCtas) : 148 * (p.vec ? 3 : 6), r)) return cudaErrorInvalidConfiguration;
+  const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * (kThr / r->G) * p.D : 0;
+  if (p.vec) {
+    constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
+    const int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>;
+    return launch_rows(p.interleaved ? qk_rows_kernel<T, Td, BWD, true> : qk_rows_kernel<T, Td, BWD, false>, p, *r,
+                       sums > ring ? sums : ring, s);
+  }
+  return launch_rows(pairs_of(p) <= 4 * r->G ? qk_pairs_kernel<T, Td, BWD, 4> : qk_pairs_kernel<T, Td, BWD, 8>, p, *r, sums, s);
 }
 
-template <typename T, int NU> cudaError_t pairs_bwd(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
-  const int G = lanes_per_row(p), per_cta = kThr / G;
-  int64_t work[2];
-  for (int j = 0; j < 2; j++) work[j] = (p.Bt * p.L * p.H[j] + per_cta - 1) / per_cta;
-  int nb1;
-  split_blocks(work, kBwdCtas, nb0, &nb1);
-  *nb = *nb0 + nb1;
-  const size_t smem = p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)per_cta * p.D : 0;
-  qk_pairs_bwd_kernel<T, NU><<<*nb, kThr, smem, s>>>(p, G, *nb0);
-  return cudaGetLastError();
-}
-
-template <typename T, int TV, int NS>
-cudaError_t time_fwd(const QkParams &p, cudaStream_t s) {
-  const TimePlan t = time_plan(p);
-  const int64_t tiles = t.tiles[0] + t.tiles[1];
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const size_t smem = sizeof(float) * kThr * TV;
-  qk_time_kernel<T, TV, NS, false><<<(unsigned)tiles, kThr, smem, s>>>(p, t.TX, 0, t.tiles[0], t.tiles[1]);
-  return cudaGetLastError();
-}
-
-template <typename T, int TV, int NS>
-cudaError_t time_bwd(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
-  const TimePlan t = time_plan(p);
-  int nb1;
-  split_blocks(t.tiles, kBwdCtas, nb0, &nb1);
-  *nb = *nb0 + nb1;
-  const size_t smem = sizeof(float) * kThr * 2 * TV;
-  qk_time_kernel<T, TV, NS, true><<<*nb, kThr, smem, s>>>(p, t.TX, *nb0, t.tiles[0], t.tiles[1]);
+// CTAs of a time_last launch: four per SM forwards, the backward's two (each keeps a share of dw of both sides).
+template <typename T, bool BWD> cudaError_t time_run(const QkParams &p, int *nb, cudaStream_t s) {
+  const TimePlan t = time_plan(p, BWD);
+  const int64_t most = BWD ? 2 * 148 : 4 * 148;
+  *nb = (int)(t.tiles < most ? t.tiles : most);
+  const int pairs = pairs_of(p), TY = kThr / t.TX;
+  const auto kernel = p.vec ? (pairs <= TY ? qk_time_kernel<T, 8, 1, BWD> : qk_time_kernel<T, 8, 8, BWD>)
+                            : (pairs <= TY       ? qk_time_kernel<T, 1, 1, BWD>
+                               : pairs <= 4 * TY ? qk_time_kernel<T, 1, 4, BWD>
+                                                 : qk_time_kernel<T, 1, 32, BWD>);
+  kernel<<<*nb, kThr, t.smem, s>>>(p, t.TX, t.heads, t.chunks, t.tiles);
   return cudaGetLastError();
 }
 
 template <typename T> cudaError_t fwd_t(const QkParams &p, cudaStream_t s) {
-  const int pairs = p.rot / 2 + (p.D - p.rot + 1) / 2;
-  if (p.time_last) {
-    if (p.vec) return pairs <= 32 ? time_fwd<T, 8, 1>(p, s) : time_fwd<T, 8, 8>(p, s);
-    return pairs <= 32 ? time_fwd<T, 1, 1>(p, s) : time_fwd<T, 1, 8>(p, s);
-  }
-  if (!p.vec) return pairs <= 128 ? pairs_fwd<T, 4>(p, s) : pairs_fwd<T, 8>(p, s);
-  int nb0, nb;
-  return p.interleaved ? rows_launch<T, T, false, true>(p, &nb0, &nb, s) : rows_launch<T, T, false, false>(p, &nb0, &nb, s);
-}
-
-template <typename T, typename Td> cudaError_t bwd_rows(const QkParams &p, int *nb0, int *nb, cudaStream_t s) {
-  return p.interleaved ? rows_launch<T, Td, true, true>(p, nb0, nb, s) : rows_launch<T, Td, true, false>(p, nb0, nb, s);
+  int nb;
+  if (p.time_last) return time_run<T, false>(p, &nb, s);
+  RowPlan r;
+  return rows_run<T, T, false>(p, &r, s);
 }
 
 template <typename T> cudaError_t bwd_t(const QkParams &p, cudaStream_t s) {
-  const int pairs = p.rot / 2 + (p.D - p.rot + 1) / 2;
-  int nb0 = 0, nb = 0;
-  cudaError_t e;
+  const bool sums = p.dw[0] || p.dw[1];
+  const dim3 grid((unsigned)((p.D + 31) / 32), 2);
   if (p.time_last) {
-    if (p.vec) e = pairs <= 32 ? time_bwd<T, 8, 1>(p, &nb0, &nb, s) : time_bwd<T, 8, 8>(p, &nb0, &nb, s);
-    else e = pairs <= 32 ? time_bwd<T, 1, 1>(p, &nb0, &nb, s) : time_bwd<T, 1, 8>(p, &nb0, &nb, s);
-  } else if (!p.vec) {
-    e = pairs <= 128 ? pairs_bwd<T, 4>(p, &nb0, &nb, s) : pairs_bwd<T, 8>(p, &nb0, &nb, s);
+    int nb;
+    const cudaError_t e = time_run<T, true>(p, &nb, s);
+    if (e != cudaSuccess || !sums) return e;
+    qk_dw_kernel<<<grid, 1024, 0, s>>>(p, nb, 1, nb, 2);
   } else {
-    e = p.dout[p.H[0] == 0].bf16 ? bwd_rows<T, __nv_bfloat16>(p, &nb0, &nb, s) : bwd_rows<T, float>(p, &nb0, &nb, s);
+    RowPlan r;
+    const cudaError_t e = p.dout[p.H[0] == 0].bf16 ? rows_run<T, __nv_bfloat16, true>(p, &r, s) : rows_run<T, float, true>(p, &r, s);
+    if (e != cudaSuccess || !sums) return e;
+    qk_dw_kernel<<<grid, 1024, 0, s>>>(p, r.nb0, r.nb0, r.nb - r.nb0, 1);
   }
-  if (e != cudaSuccess || (!p.dw[0] && !p.dw[1])) return e;
-  qk_dw_kernel<<<dim3((unsigned)((p.D + 31) / 32), 2), 1024, 0, s>>>(p, nb0, nb);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Whatever the plan: at most kBwdCtas shares, one more where a side rounds up from none.
+// Whatever the plan: at most kBwdCtas shares, one more where a side rounds up from none; two from each of 2 * 148 CTAs with
+// time innermost.
 size_t qk_bwd_workspace_bytes(const QkParams &p) {
-  return p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(kBwdCtas + 2) * (size_t)p.D : 0;
+  return p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(4 * 148) * (size_t)p.D : 0;
 }
+static_assert(kBwdCtas + 2 <= 4 * 148 && 2 * 148 <= kBwdCtas, "the workspace and the reduction hold every plan's shares");
 
 cudaError_t launch_qk_fwd(const QkParams &p, int in_bf16, cudaStream_t s) {
   return in_bf16 ? fwd_t<__nv_bfloat16>(p, s) : fwd_t<float>(p, s);
