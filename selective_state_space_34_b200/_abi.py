@@ -171,6 +171,23 @@ def load():
     return _lib
 
 
+_native = None
+
+
+def marshal():
+    """The native marshalling module (csrc/ssm_marshal.cpp). Raises if it is not built; there is no other path."""
+    global _native
+    if _native is None:
+        load()
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise ImportError("_marshal.so is not built or does not match this torch (%s); run "
+                              "`python -m selective_state_space_34_b200.build`" % e) from e
+        _native = _marshal
+    return _native
+
+
 class SSMError(RuntimeError):
     def __init__(self, fn: str, code: int):
         lib = load()

@@ -1,4 +1,5 @@
-"""Build the sm_100a selective-scan library in-tree: selective_state_space_34_b200/libssm_scan.so.
+"""Build the sm_100a selective-scan library in-tree: selective_state_space_34_b200/libssm_scan.so, and beside it the
+native marshalling module _marshal.so (csrc/ssm_marshal.cpp, against the installed torch's headers).
 
 nvcc compiles every csrc/*.cu for sm_100a (-gencode arch=compute_100a,code=sm_100a) and links a
 shared library with the CUDA runtime linked statically, so the .so has no dependency beyond the
@@ -11,11 +12,13 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libssm_scan.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 BUILD = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -38,15 +41,49 @@ def _deps():
         [os.path.join(ROOT, "include", "ssm_scan.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _marshal_deps():
+    return [os.path.join(CSRC, "ssm_marshal.cpp"), os.path.join(ROOT, "include", "ssm_scan.h")]
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile _marshal.so: plain C++ (no device code), linked to the library beside it and to torch."""
+    if not force and _newer(MARSHAL, _marshal_deps()):
+        return MARSHAL
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I" + sysconfig.get_paths()["include"], "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), os.path.join(CSRC, "ssm_marshal.cpp"), "-o", tmp,
+           "-L" + PKG, "-l:libssm_scan.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("marshalling module failed to build:\n" + r.stderr[-4000:])
+    os.replace(tmp, MARSHAL)
+    if verbose:
+        print("built", MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_marshal(verbose=verbose)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -71,6 +108,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB)
+    build_marshal(force, verbose)
     return LIB
 
 

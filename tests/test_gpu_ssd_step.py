@@ -1,11 +1,13 @@
 """The state-space-dual step against float64, continuing ssm_ssd_fwd; and the new operators run together as
 recurrent layers use them: normalised and rotated B and C in front of the scan and the dual, the gated recurrence behind."""
+import ctypes
+
 import pytest
 import torch
 
 import layer_refs as ref
 import selective_state_space_34_b200 as ssm
-from selective_state_space_34_b200 import layers
+from selective_state_space_34_b200 import _abi
 from test_gpu_guard import GuardedTorch
 
 pytestmark = pytest.mark.gpu
@@ -167,56 +169,127 @@ def test_recurrent_layer_prefill_then_decode():
         ref.check("row %d" % b, torch.stack(outs, -1)[b:b + 1], v[..., m:], (e + ref.EPS * v.abs())[..., m:])
 
 
-class Guarded(GuardedTorch):
-    """GuardedTorch for the allocations of layers.py."""
-
-    def empty_like(self, t, dtype=None, memory_format=None):
-        return self.empty(tuple(t.shape), dtype=dtype or t.dtype, device=t.device)
-
-
-def _guarded(monkeypatch, fn):
+def _guarded(fn):
+    """Run fn(allocator) twice over memory filled with two patterns, every buffer between guard bands: no byte outside a
+    buffer changes, every output element is written, and nothing read differs with the pattern."""
     results = []
     for fill in (0xA5, 0x5A):
-        gt = Guarded(fill)
-        monkeypatch.setattr(layers, "torch", gt)
-        try:
-            r = fn()
-            torch.cuda.synchronize()
-        finally:
-            monkeypatch.setattr(layers, "torch", torch)
-        gt.check()
-        results.append([v.clone() for v in r])
+        g = GuardedTorch(fill)
+        outs = fn(g)
+        torch.cuda.synchronize()
+        g.check()
+        results.append([v.clone() for v in outs])
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
-def test_guard_bands(monkeypatch):
-    """No write outside an output or a workspace, every output written, nothing read that was not written."""
+def _fill(g, args, inputs, outputs, **numbers):
+    """Copies of the inputs and fresh outputs ({name: (shape, dtype)}) in guarded buffers, their addresses in args."""
+    made = {}
+    for k, v in inputs.items():
+        if v is not None:
+            made[k] = g.empty(tuple(v.shape), dtype=v.dtype, device="cuda")
+            made[k].copy_(v)
+    for k, (shape, dtype) in outputs.items():
+        made[k] = g.empty(tuple(shape), dtype=dtype, device="cuda")
+    for k, v in made.items():
+        setattr(args, k, v.data_ptr())
+    for k, v in numbers.items():
+        setattr(args, k, v)
+    return made
+
+
+def _run(g, name, args, size=None):
+    lib = _abi.load()
+    if size is not None:
+        need = getattr(lib, size)(ctypes.byref(args))
+        if need:
+            args.workspace = g.empty((need,), dtype=torch.uint8, device="cuda").data_ptr()
+            args.workspace_bytes = need
+            assert args.workspace % 256 == 0
+    _abi.check(name, getattr(lib, name)(ctypes.byref(args), torch.cuda.current_stream().cuda_stream))
+
+
+CODE = {F32: _abi.SSM_F32, BF: _abi.SSM_BF16}
+
+
+@pytest.mark.parametrize("Bt,Dn,L,dtype", [(2, 5, 517, BF), (1, 3, 4100, F32), (3, 2, 9, BF), (2, 3, 70, F32)])
+def test_guard_bands_of_the_recurrence(Bt, Dn, L, dtype):
     from test_gpu_lru import inputs as lru_inputs
+
+    t = lru_inputs(Bt, Dn, L, dtype)
+    names = ("x", "r", "i", "lam", "r_bias", "i_bias", "h0", "lengths", "reset")
+
+    def fn(g):
+        a = _abi.LruArgs()
+        n = dict(Bt=Bt, Dn=Dn, L=L, c=8.0, in_dtype=CODE[dtype], out_dtype=CODE[dtype])
+        ns = ssm.ssm_lru_num_states(L)
+        m = _fill(g, a, {k: t[k] for k in names}, {"out": ((Bt, Dn, L), dtype), "h_last": ((Bt, Dn), F32)}, **n)
+        # states: rows that start a group early use one more than others, so only the bands are checked
+        st = g.empty((Bt * Dn * ns * 4,), dtype=torch.uint8, device="cuda")
+        a.chunk_states = st.data_ptr()
+        _run(g, "ssm_lru_fwd", a)
+        b = _abi.LruBwdArgs()
+        b.fwd = a
+        outs = {k: ((Bt, Dn, L), dtype) for k in ("dx", "dr", "di")}
+        outs.update({k: ((Dn,), F32) for k in ("dlam", "dr_bias", "di_bias")}, dh0=((Bt, Dn), F32))
+        w = _fill(g, b, {"dout": t["dout"], "dh_last": t["dh_last"]}, outs, grad_dtype=CODE[dtype])
+        _run(g, "ssm_lru_bwd", b, "ssm_lru_bwd_workspace_size")
+        b.fwd.chunk_states = None  # recomputed into the workspace
+        _run(g, "ssm_lru_bwd", b, "ssm_lru_bwd_workspace_size")
+        return [m["out"], m["h_last"]] + [w[k] for k in outs]
+
+    _guarded(fn)
+
+
+@pytest.mark.parametrize("Bt,L,Hq,Hk,D,rot,time", [
+    (2, 37, 3, 1, 80, 48, False), (1, 21, 2, 2, 33, 18, False), (1, 5, 2, 1, 128, 128, False), (2, 72, 1, 1, 16, 16, True),
+    (1, 45, 2, 1, 66, 20, True), (1, 24, 1, 1, 130, 64, True), (1, 9, 2, 1, 300, 300, True)])
+@pytest.mark.parametrize("interleaved", [0, 1])
+def test_guard_bands_of_queries_and_keys(Bt, L, Hq, Hk, D, rot, time, interleaved):
     from test_gpu_qk import freq, inputs as qk_inputs
 
-    def lru():
-        outs = []
-        for Bt, Dn, L, dtype in ((2, 5, 517, BF), (1, 3, 4100, F32), (3, 2, 9, BF)):
-            t = lru_inputs(Bt, Dn, L, dtype)
-            kw = {k: t[k] for k in ("r_bias", "i_bias", "h0", "lengths")}
-            f = ssm.ssm_lru_fwd(t["x"], t["r"], t["i"], t["lam"], return_state=True, **kw)
-            g = ssm.ssm_lru_bwd(t["dout"], t["x"], t["r"], t["i"], t["lam"], grad_dtype=dtype, **kw)
-            outs += [f["out"], f["h_last"]] + list(g.values())
-        return outs
+    t = qk_inputs(Bt, L, Hq, Hk, D, BF, time)
+    shape = {"q": t["q"].shape, "k": t["k"].shape}
 
-    def qk():
-        outs = []
-        for (Bt, L, Hq, Hk, D, rot), time in (((2, 37, 3, 1, 80, 48), False), ((1, 21, 2, 2, 33, 18), False),
-                                              ((2, 72, 1, 1, 16, 16), True), ((1, 45, 2, 1, 66, 20), True)):
-            t = qk_inputs(Bt, L, Hq, Hk, D, BF, time)
-            kw = dict(q_weight=t["q_weight"], k_weight=t["k_weight"], inv_freq=freq(rot), layout="bhdl" if time else "blhd")
-            outs += list(ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], **kw))
-            outs += list(ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], t["dk_out"], t["k"], **kw).values())
-        return outs
+    def strides(H):
+        return dict(sb=L * H * D, sh=D * L if time else D, sr=L if time else H * D)
 
-    def step():
-        t = inputs(2, 5, 96, 33, BF)
-        return [ssm.ssm_ssd_step(t["x"], t["dt"], t["A_log"], t["B"], t["C"], t["h"])]
+    def fn(g):
+        n = dict(Bt=Bt, L=L, Hq=Hq, Hk=Hk, D=D, rot=rot, eps=1e-6, rot_scale=1.0, norm=1, interleaved=interleaved, pos_i64=1,
+                 layout=int(time), in_dtype=1, out_dtype=1)
+        for side, H in (("q", Hq), ("k", Hk)):
+            for k, v in strides(H).items():
+                n["%s_%s" % (side, k)] = n["%s_out_%s" % (side, k)] = v
+        a = _abi.QkArgs()
+        ins = {k: t[k] for k in ("q", "k", "q_weight", "k_weight", "positions")}
+        m = _fill(g, a, dict(ins, inv_freq=freq(rot)), {"q_out": (shape["q"], BF), "k_out": (shape["k"], BF)}, **n)
+        _run(g, "ssm_qk_norm_rope_fwd", a)
+        b = _abi.QkBwdArgs()
+        b.fwd = a
+        n = dict(dout_dtype=1, grad_dtype=0)
+        for side, H in (("q", Hq), ("k", Hk)):
+            n.update({"d%s_%s" % (side, k): v for k, v in strides(H).items()})
+        outs = {"dq": (shape["q"], F32), "dk": (shape["k"], F32), "dq_weight": ((D,), F32), "dk_weight": ((D,), F32)}
+        w = _fill(g, b, {"dq_out": t["dq_out"], "dk_out": t["dk_out"]}, outs, **n)
+        _run(g, "ssm_qk_norm_rope_bwd", b, "ssm_qk_norm_rope_bwd_workspace_size")
+        return [m["q_out"], m["k_out"]] + [w[k] for k in outs]
 
-    for fn in (lru, qk, step):
-        _guarded(monkeypatch, fn)
+    _guarded(fn)
+
+
+@pytest.mark.parametrize("Bt,H,P,N", [(2, 5, 96, 33), (1, 2, 250, 7), (3, 1, 33, 64)])
+def test_guard_bands_of_the_steps(Bt, H, P, N):
+    t = inputs(Bt, H, P, N, BF)
+
+    def fn(g):
+        a = _abi.SsdStepArgs()
+        m = _fill(g, a, t, {"out": ((Bt, H, P), BF)}, Bt=Bt, H=H, P=P, N=N, in_dtype=1, out_dtype=1, delta_softplus=1)
+        _run(g, "ssm_ssd_step", a)
+        s = _abi.LruStepArgs()
+        x = {k: t["x"][:, 0].contiguous() for k in ("x", "r", "i")}
+        x.update(lam=t["A_log"].new_full((P,), -4.0), h=t["h"][:, 0, 0].contiguous())
+        k = _fill(g, s, x, {"out": ((Bt, P), BF)}, Bt=Bt, Dn=P, c=8.0, in_dtype=1, out_dtype=1)
+        _run(g, "ssm_lru_step", s)
+        return [m["out"], m["h"], k["out"], k["h"]]
+
+    _guarded(fn)
