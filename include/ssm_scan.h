@@ -417,7 +417,7 @@ typedef struct ssm_lru_args {
 } ssm_lru_args;
 
 /* Errors: SSM_ERR_NULL (x, r, i, lam or out NULL), SSM_ERR_SHAPE, SSM_ERR_ALIGN, SSM_ERR_DTYPE,
- * SSM_ERR_UNSUPPORTED (c, or L of 2^31 - 2^13 and more), SSM_ERR_CUDA. L = 0: h_last = h0 or 0. */
+ * SSM_ERR_UNSUPPORTED (c, or L of 2^31 - 2^15 and more), SSM_ERR_CUDA. L = 0: h_last = h0 or 0. */
 ssm_status ssm_lru_fwd(const ssm_lru_args *args, void *stream);
 
 typedef struct ssm_lru_bwd_args {

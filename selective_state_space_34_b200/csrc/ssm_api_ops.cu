@@ -13,7 +13,7 @@
 namespace {
 
 constexpr int64_t kMaxElems = INT64_C(1) << 50;
-constexpr int64_t kMaxSteps = (INT64_C(1) << 31) - (1 << 13);  // the recurrence counts a row's steps in 32 bits
+constexpr int64_t kMaxSteps = (INT64_C(1) << 31) - (1 << 15);  // the recurrence counts a row's steps in 32 bits
 
 ssm_status cuda_status(cudaError_t e) { return (ssm_status)ssm::record_cuda_error_code(e); }
 

@@ -75,30 +75,37 @@ __device__ __forceinline__ void in_order(const float2 *v, float *o) {
 
 // What a row's gates need of its parameters. A gate's argument is kept above -42 (its sigmoid above 2^-60), so
 // that the product of two denominators 1 + e^-v stays finite; NaN passes. bf16 inputs are clamped as they are, two
-// at a time (`low`, rounded to bf16, which moves the bound by a 2^-8 part at most).
+// at a time, to `low`, which rounding to bf16 moves by 2 at most while the bias is within 1024; a row with
+// a larger one (a gate held shut or open) clamps the arguments themselves, as fp32 inputs do.
 struct Gate {
   float shift;         // -bias log2 e
   __nv_bfloat162 low;  // -41.5 - bias
+  bool wide;
 };
 __device__ __forceinline__ Gate gate_of(float bias) {
-  return {-bias * kLog2e, __float2bfloat162_rn(-41.5f - bias)};
+  return {-bias * kLog2e, __float2bfloat162_rn(-41.5f - bias), !(fabsf(bias) <= 1024.f)};
+}
+__device__ __forceinline__ void clamp(float2 *t) {
+#pragma unroll
+  for (int j = 0; j < 4; j++) t[j] = make_float2(min_nan(t[j].x, 60.f), min_nan(t[j].y, 60.f));
 }
 __device__ __forceinline__ void arguments(const Raw8<__nv_bfloat16> &raw, const Gate &g, float2 *t) {
   Raw8<__nv_bfloat16> c = raw;
-  __nv_bfloat162 *w = reinterpret_cast<__nv_bfloat162 *>(&c.a);
+  if (!g.wide) {
+    __nv_bfloat162 *w = reinterpret_cast<__nv_bfloat162 *>(&c.a);
 #pragma unroll
-  for (int j = 0; j < 4; j++) w[j] = __hmax2_nan(w[j], g.low);
+    for (int j = 0; j < 4; j++) w[j] = __hmax2_nan(w[j], g.low);
+  }
   pairs(c, t);
 #pragma unroll
   for (int j = 0; j < 4; j++) t[j] = fma2(t[j], splat(-kLog2e), splat(g.shift));
+  if (g.wide) clamp(t);
 }
 __device__ __forceinline__ void arguments(const Raw8<float> &raw, const Gate &g, float2 *t) {
   pairs(raw, t);
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    t[j] = fma2(t[j], splat(-kLog2e), splat(g.shift));
-    t[j] = make_float2(min_nan(t[j].x, 60.f), min_nan(t[j].y, 60.f));
-  }
+  for (int j = 0; j < 4; j++) t[j] = fma2(t[j], splat(-kLog2e), splat(g.shift));
+  clamp(t);
 }
 // Both sigmoids from -v log2 e, with one reciprocal: 1/((1+eu)(1+ev)); ev = e^-v on the side, with which
 // 1 - sigmoid(v) = ev sigmoid(v).
@@ -140,7 +147,7 @@ __device__ __forceinline__ float decay_rate(float c, float lam) { return c * sof
 struct Row {
   int64_t flat;  // flat index of the row's first element
   int f;         // elements of its first group that belong to the row before
-  int len;       // live steps (L is below 2^31 - 2^13, so steps and chunks count in 32 bits)
+  int len;       // live steps (L is below 2^31 - 2^15, so steps and chunks count in 32 bits)
   int k_lo, k_hi;  // the chunks inside the live steps
   int n_live;      // chunks that hold live steps
 };

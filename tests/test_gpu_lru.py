@@ -159,6 +159,37 @@ def test_extreme_decays(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("big", [1100.0, 1e5, 1e9, 3e38])
+def test_gates_held_shut_or_open(dtype, big):
+    """Biases far beyond any argument: the decay gate open or shut, the input gate open or shut, exactly."""
+    L = 300
+    t = inputs(1, 4, L, dtype, seed=5)
+    t["r_bias"] = torch.tensor([big, big, -big, -big]).cuda()
+    t["i_bias"] = torch.tensor([big, -big, big, -big]).cuda()
+    t["lam"] = torch.full((4,), -2.0).cuda()
+    kw = options(t, FULL)
+    args = (t["x"], t["r"], t["i"], t["lam"])
+    f = ssm.ssm_lru_fwd(*args, save_states=True, out_dtype=F32, **kw)
+    g = ssm.ssm_lru_bwd(t["dout"], *args, chunk_states=f["chunk_states"], **kw)
+    out, x, h0 = ref.d64(f["out"])[0], ref.d64(t["x"])[0], ref.d64(t["h0"])[0]
+    assert all(bool(v.isfinite().all()) for v in [f["out"]] + list(g.values()))
+    a = torch.exp(-8.0 * ref.softplus(torch.tensor(-2.0).double()))
+    m = torch.sqrt(1 - a * a)
+    h = [h0[0], h0[1]]
+    for k in range(L):  # decay gate open: a is e^(-c softplus(lam)), the input x or none
+        h = [a * h[0] + m * x[0, k], a * h[1]]
+        assert abs(float(out[0, k] - h[0])) <= 1e-5 * (1 + abs(float(h[0]))), k
+        assert abs(float(out[1, k] - h[1])) <= 1e-5 * abs(float(h0[1])), k
+    # shut: a is 1 and nothing comes in (a shut gate reads 2^-60 at most: m is below 2^-29 of x, 300 times)
+    assert bool(((out[2:] - h0[2:, None]).abs() <= 300 * 2.0 ** -28 * 8).all())
+    step = inputs(1, 4, 1, dtype, seed=5, step=True)
+    hs = step["h0"].clone()
+    ssm.ssm_lru_step(step["x"], step["r"], step["i"], t["lam"], hs, t["r_bias"], t["i_bias"])
+    got, xs, was = ref.d64(hs)[0], ref.d64(step["x"])[0], ref.d64(step["h0"])[0]
+    assert bool((got - torch.stack([a * was[0] + m * xs[0], a * was[1], was[2], was[3]])).abs().max() <= 1e-5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_chained_chunks_equal_one_call(dtype):
     t = inputs(2, 5, 640, dtype)
     rest = (t["lam"], t["r_bias"], t["i_bias"])
