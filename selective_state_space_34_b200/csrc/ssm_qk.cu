@@ -234,11 +234,11 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   // in shared memory, by unit: the weights of its two runs, and its pairs' turns per position
   __shared__ float4 sw[4][32];
   __shared__ double sf[8][32];
-  if (threadIdx.x < p.D / 16) {
+  if (threadIdx.x < 32) {  // lanes without a unit read weights too: 1, which their zeros stay 0 with
     float2 w[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) w[j] = splat(1.f);
-    if (p.norm && p.w[side]) {
+    if ((int)threadIdx.x < p.D / 16 && p.norm && p.w[side]) {
       const int u = threadIdx.x;
       const bool h = u < ur && !INTER;
       Raw8<float> a, b;

@@ -17,6 +17,16 @@ EPS = 2.0 ** -24
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: EPS}  # half a step of a result's rounding, relative
 
 
+def poison_shared():
+    """Leave NaN in the shared memory of every SM (a call over NaN whose staging buffers and tables fill 70 KB of it), so
+    that a kernel which reads shared memory before writing it shows."""
+    import selective_state_space_34_b200 as ssm
+    q = torch.full((1, 4000, 4, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w = torch.full((512,), float("nan"), device="cuda")
+    f = torch.full((256,), float("nan"), device="cuda")
+    ssm.ssm_qk_norm_rope_bwd(q, q, q_weight=w, inv_freq=f)
+
+
 def d64(t):
     return None if t is None else t.detach().double().cpu()
 

@@ -11,6 +11,11 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def _poisoned():
+    ref.poison_shared()
+
+
 def inputs(Bt, L, Hq, Hk, D, dtype, time=False, seed=0, dout=None):
     g = torch.Generator().manual_seed(seed)
     shape = (lambda H: (Bt, H, D, L)) if time else (lambda H: (Bt, L, H, D))
@@ -160,6 +165,16 @@ def test_zero_rows_and_nan_rows():
     assert bool((q[0, 2] == 0).all()) and bool(q[0, 4, 1].isnan().all())
     keep = q[0, [0, 1, 3, 5]]
     assert bool(keep.isfinite().all()) and bool(q[0, 4, 0].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D", [48, 80, 96, 160, 208])
+def test_head_sizes_that_leave_lanes_over(D, dtype):
+    """Units of 16 that do not fill a power of two of lanes."""
+    t = inputs(2, 300, 3, 1, D, dtype, seed=D)
+    for inter in (False, True):
+        ref.poison_shared()
+        run_and_check(t, freq(D), True, inter)
 
 
 def test_empty_and_missing_sides():

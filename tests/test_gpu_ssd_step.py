@@ -14,6 +14,11 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def _poisoned():
+    ref.poison_shared()
+
+
 def inputs(Bt, H, P, N, dtype, seed=0):
     g = torch.Generator().manual_seed(seed)
     n = lambda *s, std=1.0: torch.randn(s, generator=g) * std  # noqa: E731
