@@ -197,19 +197,13 @@ ssm::QkParams qk_params(const ssm_qk_args *a) {
   return p;
 }
 
-// 16-byte accesses: every tensor of a side with heads starts on a 16-byte boundary and steps by multiples of 8
-// elements; with head elements innermost the units of 16 must also tile the head, and of the half layout the rotated part.
+// Time innermost: every tensor of a side with heads starts on a 16-byte boundary and steps by multiples of 8 elements.
 bool qk_vec_ok(const ssm::QkParams &p) {
-  if (!p.time_last && (p.D % 16 != 0 || (!p.interleaved && p.rot % 16 != 0))) return false;
-  const int64_t rows = p.time_last ? p.D : p.L;
   for (int s = 0; s < 2; s++) {
     if (p.H[s] == 0) continue;
-    if (!p.time_last && !aligned(p.w[s], 16)) return false;
-    const ssm::QkTensor *const ts[3] = {&p.in[s], &p.out[s], &p.dout[s]};
-    for (const ssm::QkTensor *t : ts) {
+    for (const ssm::QkTensor *t : {&p.in[s], &p.out[s], &p.dout[s]}) {
       if (!t->p) continue;
-      if (!aligned(t->p, 16) || (p.Bt > 1 && t->sb % 8 != 0) || (p.H[s] > 1 && t->sh % 8 != 0) ||
-          (rows > 1 && t->sr % 8 != 0))
+      if (!aligned(t->p, 16) || (p.Bt > 1 && t->sb % 8 != 0) || (p.H[s] > 1 && t->sh % 8 != 0) || (p.D > 1 && t->sr % 8 != 0))
         return false;
     }
   }
@@ -249,7 +243,7 @@ ssm::QkParams qk_bwd_params(const ssm_qk_bwd_args *a) {
   p.out[1] = tensor(a->dk, a->dk_sb, a->dk_sh, a->dk_sr, a->grad_dtype);
   p.dw[0] = f->Hq > 0 ? a->dq_weight : nullptr;
   p.dw[1] = f->Hk > 0 ? a->dk_weight : nullptr;
-  p.vec = qk_vec_ok(p);
+  p.vec = p.time_last && qk_vec_ok(p);
   return p;
 }
 
@@ -391,7 +385,7 @@ ssm_status ssm_qk_norm_rope_fwd(const ssm_qk_args *args, void *stream) {
   ssm::QkParams p = qk_params(args);
   p.out[0] = tensor(args->q_out, args->q_out_sb, args->q_out_sh, args->q_out_sr, args->out_dtype);
   p.out[1] = tensor(args->k_out, args->k_out_sb, args->k_out_sh, args->k_out_sr, args->out_dtype);
-  p.vec = qk_vec_ok(p);
+  p.vec = p.time_last && qk_vec_ok(p);
   return cuda_status(ssm::launch_qk_fwd(p, args->in_dtype == SSM_BF16, static_cast<cudaStream_t>(stream)));
 }
 

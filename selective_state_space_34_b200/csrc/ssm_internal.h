@@ -187,7 +187,7 @@ struct QkParams {
   int64_t Bt, L;
   int H[2], D, rot;
   int freq_f64, pos_i64, interleaved, norm, time_last;
-  int vec;                   // 16-byte accesses: see qk_vec_ok in ssm_api_ops.cu
+  int vec;                   // time_last: 16-byte accesses
   float eps, rot_scale, inv_D;  // inv_D = 1 / D
 };
 cudaError_t launch_qk_fwd(const QkParams &p, int in_bf16, cudaStream_t stream);

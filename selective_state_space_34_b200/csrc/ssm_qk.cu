@@ -15,12 +15,14 @@
 // no exchange between lanes. G lanes hold a row (G = units rounded up to a power of two) and add
 // its squares by shuffles. Head sizes, strides or alignments that do not fit take units of one pair.
 //
-// Time innermost (time_last): a thread owns consecutive steps of a pair and walks the heads with one set of cosines and
-// sines; the squares of a step meet in shared memory.
+// Time innermost (time_last): a warp owns 32 consecutive steps and walks the pairs and heads, two heads on one set of cosines
+// and sines; a step's squares meet by shuffles.
 //
 // Angles. In 32 bits position * inv_freq loses the angle of a far position (at 10^6 the spacing is 1/16 of
 // a radian), so the product and its reduction to a fraction of a turn are in 64 bits; what is left
 // goes through the hardware sine (absolute error 2^-21) for bf16, sincospif for fp32 inputs.
+#include <type_traits>
+
 #include "ssm_internal.h"
 #include "ssm_vec.cuh"
 
@@ -30,7 +32,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThr = 256;                 // threads per CTA
-constexpr int kBwdCtas = 148 * 3;         // most CTAs of a backward (each keeps a share of dw)
+constexpr int kBwdCtas = 148 * 2;         // most CTAs of a backward (each keeps a share of dw)
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 __device__ __forceinline__ float ld1(const void *p, int bf16, int64_t i) {
@@ -39,17 +41,6 @@ __device__ __forceinline__ float ld1(const void *p, int bf16, int64_t i) {
 __device__ __forceinline__ void st1(void *p, int bf16, int64_t i, float v) {
   if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<float *>(p)[i] = v;
-}
-__device__ __forceinline__ void ld8any(const void *p, int bf16, int64_t i, float *v) {
-  if (bf16) {
-    Raw8<__nv_bfloat16> r;
-    ld8(static_cast<const __nv_bfloat16 *>(p) + i, r);
-    unpack8(r, v);
-  } else {
-    Raw8<float> r;
-    ld8(static_cast<const float *>(p) + i, r);
-    unpack8(r, v);
-  }
 }
 __device__ __forceinline__ void st8any(void *p, int bf16, int64_t i, const float *v) {
   if (bf16) st8(static_cast<__nv_bfloat16 *>(p) + i, v);
@@ -123,9 +114,8 @@ template <bool INTER, typename T> __device__ __forceinline__ void runs(const Raw
     s[j] = INTER ? make_float2(v[4 * j + 1], v[4 * j + 3]) : make_float2(v[8 + 2 * j], v[8 + 2 * j + 1]);
   }
 }
-template <bool INTER>
-__device__ __forceinline__ void store_runs(void *p, int bf16, int64_t o1, int64_t o2, const float2 *f, const float2 *s) {
-  float v[16];
+// Back to the order of memory: the first run, then the second.
+template <bool INTER> __device__ __forceinline__ void in_order(const float2 *f, const float2 *s, float *v) {
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     v[INTER ? 4 * j : 2 * j] = f[j].x;
@@ -133,8 +123,41 @@ __device__ __forceinline__ void store_runs(void *p, int bf16, int64_t o1, int64_
     v[INTER ? 4 * j + 1 : 8 + 2 * j] = s[j].x;
     v[INTER ? 4 * j + 3 : 8 + 2 * j + 1] = s[j].y;
   }
-  st8any(p, bf16, o1, v);
-  st8any(p, bf16, o2, v + 8);
+}
+// The first n of 8 elements in pieces of V.
+template <typename T, int V> __device__ __forceinline__ void store_pieces(T *p, const float *v, int n) {
+  if constexpr (V == 8) {
+    if (n == 8) st8(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e += V) {
+      if (e >= n) break;
+      if constexpr (V == 1) {
+        p[e] = from_f32<T>(v[e]);
+      } else if constexpr (sizeof(T) == 2) {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; j++) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[e + 2 * j], v[e + 2 * j + 1]);
+          w[j] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        if constexpr (V == 4) *reinterpret_cast<uint2 *>(p + e) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(p + e) = w[0];
+      } else {
+        if constexpr (V == 4) *reinterpret_cast<float4 *>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        else *reinterpret_cast<float2 *>(p + e) = make_float2(v[e], v[e + 1]);
+      }
+    }
+  }
+}
+// N bytes on their way to shared memory.
+template <int N> __device__ __forceinline__ void cp_async_piece(void *dst, const void *src) {
+  if constexpr (N == 16) {
+    cp_async16(dst, src);
+  } else {
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(src), "n"(N));
+  }
 }
 
 // n / d and the remainder, in 32 bits where both fit.
@@ -204,11 +227,12 @@ template <typename... F> __device__ __forceinline__ void sum_lanes(int G, F &...
   }
 }
 
-// Rows in 16-byte runs. CTAs [0, nb0) take the queries, the others the keys; a warp takes `per` consecutive rows
-// of its side, 32 / G at a time (G lanes a row, a unit of 16 elements each), and the rows ahead travel in a ring of
-// cp.async slots that every lane fills and reads alone. Cosines and sines are recomputed where the token
-// changes; a unit that is not rotated keeps 1 and 0. The backward adds its share of dw over all its rows.
-template <typename T, typename Td, bool BWD, bool INTER>
+// Rows in runs that start at multiples of V elements. CTAs [0, nb0) take the queries, the others the keys; a warp takes `per`
+// consecutive rows of its side, 32 / G at a time (G lanes a row, a unit of up to 16 elements each), and the rows ahead
+// travel in a ring of cp.async slots that every lane fills, in pieces of V elements, and reads alone. Cosines and sines are
+// recomputed where the token changes; pairs that are not rotated keep 1 and 0. The backward adds its share of dw over all its
+// rows.
+template <typename T, typename Td, bool BWD, bool INTER, int V>
 __global__ void __launch_bounds__(kThr, BWD ? 2 : 3)
 qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0, int64_t per1) {
   constexpr bool PRECISE = sizeof(T) == 4;
@@ -226,28 +250,37 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   const int64_t total = p.Bt * p.L * H;
   const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
   const int dt = step / H, dh = step % H;
-  // the lane's unit; the interleaved layout may turn some of a unit's pairs
-  const int ur = INTER ? (p.rot + 15) / 16 : p.rot / 16, turned = p.rot / 2 - 8 * sub;
-  const bool on = sub < p.D / 16, rot = sub < ur;
-  const bool half = rot && !INTER;
-  const int o1 = half ? 8 * sub : 16 * sub, o2 = half ? p.rot / 2 + 8 * sub : o1 + 8;
-  // in shared memory, by unit: the weights of its two runs, and its pairs' turns per position
+  // unit u: two runs, of n1 elements at o1 and n2 at o2. Half layout: the first and the second members of 8 pairs (fewer in the
+  // last such unit), then 16 elements a unit behind the rotated part; interleaved: 16 elements a unit.
+  const int ur = (p.rot / 2 + 7) / 8, half_rot = p.rot / 2;
+  auto unit = [&](int u, int &o1, int &o2, int &n1, int &n2) {
+    if (!INTER && u < ur) {
+      o1 = 8 * u;
+      o2 = half_rot + o1;
+      n1 = n2 = min(8, half_rot - o1);
+    } else {
+      o1 = INTER ? 16 * u : p.rot + 16 * (u - ur);
+      o2 = o1 + 8;
+      n1 = max(0, min(8, p.D - o1));
+      n2 = max(0, min(8, p.D - o2));
+    }
+  };
+  int o1, o2, n1, n2;
+  unit(sub, o1, o2, n1, n2);
+  const bool on = n1 > 0, rot = sub < ur;
+  const int turned = half_rot - 8 * sub;  // rotated pairs of the unit
+  constexpr bool kAll = !INTER && V == 8;  // all 8 of a rotated unit (the half layout's run starts are then multiples of 8)
+  // in shared memory, by unit: the weights of its pairs' members, and its pairs' turns per position
   __shared__ float4 sw[4][32];
   __shared__ double sf[8][32];
-  if (threadIdx.x < 32) {  // lanes without a unit read weights too: 1, which their zeros stay 0 with
-    float2 w[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) w[j] = splat(1.f);
-    if ((int)threadIdx.x < p.D / 16 && p.norm && p.w[side]) {
-      const int u = threadIdx.x;
-      const bool h = u < ur && !INTER;
-      Raw8<float> a, b;
-      ld8(p.w[side] + (h ? 8 * u : 16 * u), a);
-      ld8(p.w[side] + (h ? p.rot / 2 + 8 * u : 16 * u + 8), b);
-      runs<INTER>(a, b, w, w + 4);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) sw[j][threadIdx.x] = make_float4(w[2 * j].x, w[2 * j].y, w[2 * j + 1].x, w[2 * j + 1].y);
+  for (int j = threadIdx.x; j < 16 * G; j += kThr) {  // lanes without a unit read weights too: 1, which their zeros stay 0 with
+    const int u = j >> 4, e = j & 15;
+    int a1, a2, m1, m2;
+    unit(u, a1, a2, m1, m2);
+    const int at = e < 8 ? a1 + e : a2 + e - 8;
+    const bool has = p.norm && p.w[side] && (e < 8 ? e < m1 : e - 8 < m2);
+    const int k = INTER ? (e & 1) * 8 + e / 2 : e;  // first members of the 8 pairs, then second ones
+    reinterpret_cast<float *>(&sw[k >> 2][u])[k & 3] = has ? p.w[side][at] : 1.f;
   }
   for (int j = threadIdx.x; j < p.rot / 2; j += kThr) sf[j & 7][j >> 3] = frequency(p, j);
   float2 d1[4], d2[4], c[4], s[4];
@@ -262,12 +295,20 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
 #pragma unroll
     for (int k = 0; k < kSlots; k++) *reinterpret_cast<uint4 *>(slot(stage, k)) = make_uint4(0, 0, 0, 0);
   };
-  if (!on) {  // lanes without a unit hold zeros throughout
+  if (n1 < 8 || n2 < 8) {  // what a unit lacks is 0 throughout
 #pragma unroll
     for (int j = 0; j < S; j++) clear(j);
   }
   const bool reads_v = !BWD || p.norm;
   const int gap = o2 - o1;
+  // n elements at src into the slots from k on
+  auto copy = [&](int stage, int k, const auto *src, int n) {
+    constexpr int es = sizeof(*src), bytes = V * es < 16 ? V * es : 16;
+#pragma unroll
+    for (int j = 0; j < 8 * es / bytes; j++)
+      if (V == 8 ? n == 8 : j * (bytes / es) < n)
+        cp_async_piece<bytes>(slot(stage, k + j * bytes / 16) + j * bytes % 16, reinterpret_cast<const char *>(src) + j * bytes);
+  };
   Walk ahead, now;
   int64_t b0;
   ahead.start(first + grp, H, L, b0);
@@ -276,23 +317,15 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   int left = n_rows - grp;  // rows of this group still to be asked for, times step
   auto fetch = [&](int stage) {
     if (left > 0) {
-      if (on) {
-        if (reads_v) {
-          const T *a = static_cast<const T *>(in.p) + from.at, *b = a + gap;
-#pragma unroll
-          for (int k = 0; k < kSlotsV / 2; k++) {
-            cp_async16(slot(stage, k), reinterpret_cast<const char *>(a) + 16 * k);
-            cp_async16(slot(stage, kSlotsV / 2 + k), reinterpret_cast<const char *>(b) + 16 * k);
-          }
-        }
-        if (BWD) {
-          const Td *a = static_cast<const Td *>(dout.p) + dfrom.at, *b = a + gap;
-#pragma unroll
-          for (int k = 0; k < kSlotsG / 2; k++) {
-            cp_async16(slot(stage, kSlotsV + k), reinterpret_cast<const char *>(a) + 16 * k);
-            cp_async16(slot(stage, kSlotsV + kSlotsG / 2 + k), reinterpret_cast<const char *>(b) + 16 * k);
-          }
-        }
+      if (reads_v) {
+        const T *a = static_cast<const T *>(in.p) + from.at;
+        copy(stage, 0, a, n1);
+        copy(stage, kSlotsV / 2, a + gap, n2);
+      }
+      if (BWD) {
+        const Td *a = static_cast<const Td *>(dout.p) + dfrom.at;
+        copy(stage, kSlotsV, a, n1);
+        copy(stage, kSlotsV + kSlotsG / 2, a + gap, n2);
       }
       left -= step;
       if (BWD) advance(ahead, dt, dh, H, L, from, dfrom);
@@ -320,6 +353,19 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
     w[2] = make_float2(b.x, b.y);
     w[3] = make_float2(b.z, b.w);
   };
+  auto store = [&](const float2 *f, const float2 *s) {
+    float v[16];
+    in_order<INTER>(f, s, v);
+    if (out.bf16) {
+      __nv_bfloat16 *q = static_cast<__nv_bfloat16 *>(out.p) + to.at;
+      store_pieces<__nv_bfloat16, V>(q, v, n1);
+      store_pieces<__nv_bfloat16, V>(q + gap, v + 8, n2);
+    } else {
+      float *q = static_cast<float *>(out.p) + to.at;
+      store_pieces<float, V>(q, v, n1);
+      store_pieces<float, V>(q + gap, v + 8, n2);
+    }
+  };
   __syncthreads();
   int stage = 0;
   bool fresh = true;
@@ -330,8 +376,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
       const double pos = position(p, now.token, now.t);
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        if (!INTER || 2 * j < turned) turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
-        if (!INTER || 2 * j + 1 < turned) turn<PRECISE>(pos, sf[2 * j + 1][sub], p.rot_scale, c[j].y, s[j].y);
+        if (kAll || 2 * j < turned) turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
+        if (kAll || 2 * j + 1 < turned) turn<PRECISE>(pos, sf[2 * j + 1][sub], p.rot_scale, c[j].y, s[j].y);
       }
     }
     cp_async_wait<S - 1>();
@@ -379,7 +425,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
           g2[j] = fma2(v2[j], k2, mul2(gw2[j], sc2));
         }
       }
-      if (out.p && on && live) store_runs<INTER>(out.p, out.bf16, to.at, to.at + gap, g1, g2);
+      if (out.p && on && live) store(g1, g2);
     } else {
       if (p.norm) {
         float2 s2 = splat(0.f);
@@ -405,25 +451,24 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
         v1[j] = fma2(y, neg2(s[j]), mul2(x, c[j]));
         v2[j] = fma2(x, s[j], mul2(y, c[j]));
       }
-      if (on && live) store_runs<INTER>(out.p, out.bf16, to.at, to.at + gap, v1, v2);
+      if (on && live) store(v1, v2);
     }
     stage = stage == S - 1 ? 0 : stage + 1;
     fresh = advance(now, dt, dh, H, L, to);
   }
-  if (!BWD || !p.dw[side]) return;
+  if constexpr (!BWD) return;
+  if (!p.dw[side]) return;
   // the block's share of dw: the groups' in their order
   cp_async_wait<0>();
   __syncthreads();
   float *const sums = reinterpret_cast<float *>(smem);
-  if (on) {
-    float *row = sums + (threadIdx.x / G) * p.D;
+  float v[16];
+  in_order<INTER>(d1, d2, v);
+  float *row = sums + (threadIdx.x / G) * p.D;
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      row[INTER ? o1 + 4 * j : o1 + 2 * j] = d1[j].x;
-      row[INTER ? o1 + 4 * j + 2 : o1 + 2 * j + 1] = d1[j].y;
-      row[INTER ? o1 + 4 * j + 1 : o2 + 2 * j] = d2[j].x;
-      row[INTER ? o1 + 4 * j + 3 : o2 + 2 * j + 1] = d2[j].y;
-    }
+  for (int e = 0; e < 8; e++) {
+    if (e < n1) row[o1 + e] = v[e];
+    if (e < n2) row[o2 + e] = v[8 + e];
   }
   __syncthreads();
   for (int j = threadIdx.x; j < p.D; j += kThr) {
@@ -433,10 +478,10 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   }
 }
 
-// Any head size, stride and alignment: units of one pair, NU a lane, over the same walk; the next row's elements are
-// loaded into registers while a row is worked on.
+// What is left (odd head sizes, bf16 tensors off the 4-byte boundary, more units than lanes), over the same walk: units of one
+// pair, NU a lane, the next row's loaded into registers while a row is worked on.
 template <typename T, typename Td, bool BWD, int NU>
-__global__ void __launch_bounds__(kThr)
+__global__ void __launch_bounds__(kThr, NU == 8 ? 1 : BWD ? 2 : 3)
 qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0, int64_t per1) {
   constexpr bool PRECISE = sizeof(T) == 4;
   extern __shared__ float sdw[];  // (groups, D) sums of dw
@@ -451,7 +496,7 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
   const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
   const int dt = step / H, dh = step % H;
   const bool reads_v = !BWD || p.norm;
-  // the lane's units: first element, distance to the second (0: none), weights, sums of dw
+  // the lane's units: first run, distance to the second (0: none, at an odd end), weights, sums of dw
   int o[NU], gap[NU];
   bool on[NU], rot[NU];
   float w[NU][2], dw[NU][2], c[NU], s[NU];
@@ -459,12 +504,12 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
   for (int n = 0; n < NU; n++) {
     const Unit u = unit_of(p, sub + n * G);
     on[n] = u.on;
-    rot[n] = u.on && u.rot;
+    rot[n] = u.rot;
     o[n] = u.o1;
     gap[n] = u.o2 < p.D ? u.o2 - u.o1 : 0;
     w[n][0] = w[n][1] = c[n] = 1.f;
     dw[n][0] = dw[n][1] = s[n] = 0.f;
-    if (p.norm && p.w[side] && u.on) {
+    if (p.norm && p.w[side] && on[n]) {
       w[n][0] = p.w[side][u.o1];
       if (gap[n]) w[n][1] = p.w[side][u.o2];
     }
@@ -507,9 +552,9 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
 #pragma unroll
     for (int n = 0; n < NU; n++)
 #pragma unroll
-      for (int e = 0; e < 2; e++) {
-        v[n][e] = to_f32(nv[n][e]);
-        if (BWD) g[n][e] = to_f32(ng[n][e]);
+      for (int r = 0; r < 2; r++) {
+        v[n][r] = to_f32(nv[n][r]);
+        if (BWD) g[n][r] = to_f32(ng[n][r]);
       }
     fetch();
     if (fresh && live && p.rot) {
@@ -557,242 +602,487 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
     }
     fresh = advance(now, dt, dh, H, L, to);
   }
-  if (!BWD || !p.dw[side]) return;
-  // the block's share of dw: the groups' in their order
+  if constexpr (BWD) {
+    if (!p.dw[side]) return;
+    // the block's share of dw: the groups' in their order
 #pragma unroll
-  for (int n = 0; n < NU; n++)
-    if (on[n]) {
-      float *row = sdw + (threadIdx.x / G) * p.D + o[n];
-      row[0] = dw[n][0];
-      if (gap[n]) row[gap[n]] = dw[n][1];
+    for (int n = 0; n < NU; n++)
+      if (on[n]) {
+        float *row = sdw + (threadIdx.x / G) * p.D + o[n];
+        row[0] = dw[n][0];
+        if (gap[n]) row[gap[n]] = dw[n][1];
+      }
+    __syncthreads();
+    for (int j = threadIdx.x; j < p.D; j += kThr) {
+      float t = 0.f;
+      for (int r = 0; r < kThr / G; r++) t += sdw[r * p.D + j];
+      p.part[(int64_t)blockIdx.x * p.D + j] = t;
     }
-  __syncthreads();
-  for (int j = threadIdx.x; j < p.D; j += kThr) {
-    float t = 0.f;
-    for (int r = 0; r < kThr / G; r++) t += sdw[r * p.D + j];
-    p.part[(int64_t)blockIdx.x * p.D + j] = t;
   }
 }
 
 // ---- time innermost ----------------------------------------------------------------------------
 
-// m of the TV consecutive elements at i.
-template <int TV> __device__ __forceinline__ void get_run(const void *p, int bf16, int64_t i, int m, float *v) {
-  if constexpr (TV == 8) {
-    if (m == 8) {
-      ld8any(p, bf16, i, v);
-      return;
+// m of 8 consecutive elements at i, 0 behind them; 16-byte accesses where the rows allow them and all 8 live.
+__device__ __forceinline__ void get_run(const void *p, int bf16, int64_t i, int m, int vec, float *v) {
+  if (vec && m == 8) {
+    if (bf16) {  // cached: read again for the second pass
+      Raw8<__nv_bfloat16> r;
+      r.a = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+      unpack8(r, v);
+    } else {
+      Raw8<float> r;
+      ld8(static_cast<const float *>(p) + i, r);
+      unpack8(r, v);
     }
+    return;
   }
 #pragma unroll
-  for (int e = 0; e < TV; e++) v[e] = e < m ? ld1(p, bf16, i + e) : 0.f;
+  for (int e = 0; e < 8; e++) v[e] = e < m ? ld1(p, bf16, i + e) : 0.f;
 }
-template <int TV> __device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, const float *v) {
-  if constexpr (TV == 8) {
-    if (m == 8) {
-      st8any(p, bf16, i, v);
-      return;
-    }
+__device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, int vec, const float *v) {
+  if (vec && m == 8) {
+    st8any(p, bf16, i, v);
+    return;
   }
 #pragma unroll
-  for (int e = 0; e < TV; e++)
+  for (int e = 0; e < 8; e++)
     if (e < m) st1(p, bf16, i + e, v[e]);
 }
-
-// A tile is TX * TV steps of one batch element and a chunk of its heads (queries, then keys). A thread owns TV
-// consecutive steps (8 where rows are whole 16-byte runs, else 1) of NS pairs, every TY-th, TY = kThr / TX; a
-// pair unit is elements o1 and o2 (or o1 alone at an odd end). The squares of a step meet in shared memory. With one
-// pair a thread the elements stay in registers and its cosines and sines serve every head of the chunk; with more
-// the elements are read a second time, from L1.
-template <typename T, int TV, int NS, bool BWD>
-__global__ void __launch_bounds__(kThr)
-qk_time_kernel(const __grid_constant__ QkParams p, int TX, int heads, int64_t chunks, int64_t tiles) {
+// Sums of 8 values over the 8 lanes of a warp that share bits 0 and 1 of their number, every lane ending with the sum of one
+// value (7 exchanges in place of 24).
+__device__ __forceinline__ float scatter_sum(int lane, const float *v) {
+  float a[4], b[2];
+  const bool h4 = lane & 16, h2 = lane & 8, h1 = lane & 4;
+#pragma unroll
+  for (int e = 0; e < 4; e++) a[e] = (h4 ? v[e + 4] : v[e]) + __shfl_xor_sync(kFull, h4 ? v[e] : v[e + 4], 16);
+#pragma unroll
+  for (int e = 0; e < 2; e++) b[e] = (h2 ? a[e + 2] : a[e]) + __shfl_xor_sync(kFull, h2 ? a[e] : a[e + 2], 8);
+  return (h1 ? b[1] : b[0]) + __shfl_xor_sync(kFull, h1 ? b[0] : b[1], 4);
+}
+// A warp takes 32 steps of one batch element for a chunk of its heads (queries, then keys), two heads at a time: 4 lanes
+// of 8 consecutive steps, 8 lanes over the pairs, every eighth pair a lane. No barrier: a step's squares meet by shuffles.
+// Two passes over the pairs, the second from L1: the sums, then the results, with one set of cosines and sines for both
+// heads (kept over both passes and all heads where a lane has one pair, ONE). A pair unit is elements o1 and o2 (or o1
+// alone at an odd end). The backward keeps dw per warp in shared memory, each lane its own pairs'.
+template <typename T, bool BWD, bool ONE>
+__global__ void __launch_bounds__(kThr, BWD ? 2 : 3)
+qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, int64_t items) {
   constexpr bool PRECISE = sizeof(T) == 4;
-  extern __shared__ __align__(16) float sh[];
-  const int TY = kThr / TX, tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-  const int span = TX * TV, per_row = (int)((p.L + span - 1) / span);
-  // R threads add the squares of one step; rows of sh are padded so that they hit different banks
-  const int R = span < kThr ? kThr / span : 1, pitch = span + 32 / R;
-  float *const sums = sh, *const dots = sh + TY * pitch, *const res = sh + (BWD ? 2 : 1) * TY * pitch, *const res2 = res + span;
-  const int n_units = p.rot / 2 + (p.D - p.rot + 1) / 2, all = p.H[0] + p.H[1];
-  float dw[2][NS][2];
-#pragma unroll
-  for (int n = 0; n < NS; n++) dw[0][n][0] = dw[0][n][1] = dw[1][n][0] = dw[1][n][1] = 0.f;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  extern __shared__ float sdw[];  // (warps, 2, D) with dw
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane & 3, pl = lane >> 2;
+  const int n_units = p.rot / 2 + (p.D - p.rot + 1) / 2, all = p.H[0] + p.H[1], vec = p.vec;
+  const bool sums = BWD && p.norm && (p.dw[0] || p.dw[1]);
+  if (sums) {
+    for (int j = threadIdx.x; j < kThr / 32 * 2 * p.D; j += kThr) sdw[j] = 0.f;
+    __syncthreads();
+  }
+  float *const mine = sdw + warp * 2 * p.D;
+  // per warp: the positions of its 32 steps, and for each of two heads their 1 / rms and factors of the input's part of a gradient
+  __shared__ double positions[kThr / 32][32];
+  __shared__ __align__(16) float factors[kThr / 32][BWD ? 4 : 2][32];
+  double *const pos = positions[warp];
+  const int own = 8 * tl + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);  // the step whose sum this lane ends with
+  auto factor = [&](int k, float *v) {
+    const float4 *f = reinterpret_cast<const float4 *>(&factors[warp][k][8 * tl]);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  };
+  const int64_t per_row = (p.L + 31) / 32;
+  for (int64_t item = (int64_t)blockIdx.x * (kThr / 32) + warp; item < items; item += (int64_t)gridDim.x * (kThr / 32)) {
     int64_t bc, tt, b, chunk;
-    divide(tile, per_row, bc, tt);
+    divide(item, per_row, bc, tt);
     divide(bc, chunks, b, chunk);
-    const int64_t t0 = tt * span + (int64_t)tx * TV;
-    const int m = (int)(p.L - t0 < 0 ? 0 : p.L - t0 < TV ? p.L - t0 : TV);  // live steps of this thread
-    float cs[TV], sn[TV];
-    auto angles = [&](const Unit &u, int unit) {
-      const double f = u.rot ? frequency(p, unit) : 0.0;
+    const int64_t t0 = tt * 32 + 8 * tl;
+    const int m = (int)(p.L - t0 < 0 ? 0 : p.L - t0 < 8 ? p.L - t0 : 8);  // live steps of this lane
+    const int64_t t_own = tt * 32 + lane;
+    __syncwarp();  // the item before is done with them
+    pos[lane] = p.rot && t_own < p.L ? position(p, b * p.L + t_own, t_own) : 0.0;
+    __syncwarp();
+    float cs[8], sn[8];
+    auto angles = [&](int unit, bool rot) {
+      const double f = rot ? frequency(p, unit) : 0.0;
 #pragma unroll
-      for (int e = 0; e < TV; e++) {
+      for (int e = 0; e < 8; e++) {
         cs[e] = 1.f;
         sn[e] = 0.f;
-        if (u.rot && e < m) turn<PRECISE>(position(p, b * p.L + t0 + e, t0 + e), f, p.rot_scale, cs[e], sn[e]);
+        if (rot) turn<PRECISE>(pos[8 * tl + e], f, p.rot_scale, cs[e], sn[e]);
       }
     };
-    if (NS == 1) angles(unit_of(p, ty), ty);
+    if (ONE && pl < n_units) angles(pl, unit_of(p, pl).rot);
     const int h_end = min(all, (int)(chunk + 1) * heads);
-    for (int hh = (int)chunk * heads; hh < h_end; hh++) {
-      const int sd = hh >= p.H[0], h = sd ? hh - p.H[0] : hh;
-      const QkTensor &in = p.in[sd], &out = p.out[sd], &dout = p.dout[sd];
-      const int64_t at = b * in.sb + h * in.sh + t0, dat = BWD ? b * dout.sb + h * dout.sh + t0 : 0;
-      const int64_t oat = b * out.sb + h * out.sh + t0;
-      float a[TV], c[TV], ga[TV], gc[TV];  // the elements of a pair, and their gradients turned back
-      auto fetch = [&](const Unit &u, int unit) {
-        const int m2 = u.o2 < p.D ? m : 0;
-        if (!BWD || p.norm) {
-          get_run<TV>(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m, a);
-          get_run<TV>(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, m2, c);
-        }
-        if (BWD) {
-          get_run<TV>(dout.p, dout.bf16, dat + u.o1 * dout.sr, m, ga);
-          get_run<TV>(dout.p, dout.bf16, dat + u.o2 * dout.sr, m2, gc);
-          if (NS > 1) angles(u, unit);
-#pragma unroll
-          for (int e = 0; e < TV; e++) {
-            const float x = ga[e], y = gc[e];
-            ga[e] = x * cs[e] + y * sn[e];
-            gc[e] = y * cs[e] - x * sn[e];
-          }
-        }
-      };
-      const float *w = p.w[sd];
-      float sc[TV], back[TV];
-#pragma unroll
-      for (int e = 0; e < TV; e++) sc[e] = back[e] = 0.f;
+    for (int h0 = (int)chunk * heads; h0 < h_end; h0 += 2) {
+      const int nh = min(2, h_end - h0);
+      // pass 1: the squares, and backwards the products with the gradients turned back
       if (p.norm) {
+        __syncwarp();  // the heads before are done with the factors
+#pragma unroll 1
+        for (int k = 0; k < nh; k++) {
+          const int sd = h0 + k >= p.H[0], h = h0 + k - (sd ? p.H[0] : 0);
+          const QkTensor &in = p.in[sd], &dout = p.dout[sd];
+          const int64_t at = b * in.sb + h * in.sh + t0, dat = BWD ? b * dout.sb + h * dout.sh + t0 : 0;
+          const float *w = p.w[sd];
+          float sc[8], back[8];
 #pragma unroll
-        for (int n = 0; n < NS; n++) {
-          const int unit = ty + n * TY;
-          if (unit < n_units) {
+          for (int e = 0; e < 8; e++) sc[e] = back[e] = 0.f;
+          for (int unit = pl; unit < n_units; unit += 8) {
             const Unit u = unit_of(p, unit);
-            fetch(u, unit);
-            const float wa = BWD ? (w ? w[u.o1] : 1.f) : 0.f, wc = BWD && u.o2 < p.D ? (w ? w[u.o2] : 1.f) : 0.f;
+            const int m2 = u.o2 < p.D ? m : 0;
+            float a[8], c[8];
+            get_run(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m, vec, a);
+            get_run(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, m2, vec, c);
 #pragma unroll
-            for (int e = 0; e < TV; e++) {
-              sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
-              if (BWD) back[e] = fmaf(ga[e] * wa, a[e], fmaf(gc[e] * wc, c[e], back[e]));
+            for (int e = 0; e < 8; e++) sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
+            if (BWD) {
+              if (!ONE) angles(unit, u.rot);
+              const float wa = w ? w[u.o1] : 1.f, wc = w && m2 ? w[u.o2] : 1.f;
+              float ga[8], gc[8];
+              get_run(dout.p, dout.bf16, dat + u.o1 * dout.sr, m, vec, ga);
+              get_run(dout.p, dout.bf16, dat + u.o2 * dout.sr, m2, vec, gc);
+#pragma unroll
+              for (int e = 0; e < 8; e++) {
+                const float x = ga[e] * cs[e] + gc[e] * sn[e], y = gc[e] * cs[e] - ga[e] * sn[e];
+                back[e] = fmaf(x * wa, a[e], fmaf(y * wc, c[e], back[e]));
+              }
             }
           }
+          const float r = inv_rms(p, scatter_sum(lane, sc));
+          factors[warp][k][own] = r;
+          if (BWD) factors[warp][2 + k][own] = r * r * scatter_sum(lane, back) * p.inv_D;
         }
-        // every thread's partial sums, then a step's over its TY threads in a fixed order
-        if constexpr (TV == 8) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            *reinterpret_cast<float4 *>(sums + ty * pitch + tx * 8 + e) = make_float4(sc[e], sc[e + 1], sc[e + 2], sc[e + 3]);
-            if (BWD)
-              *reinterpret_cast<float4 *>(dots + ty * pitch + tx * 8 + e) = make_float4(back[e], back[e + 1], back[e + 2], back[e + 3]);
-          }
-        } else {
-          sums[ty * pitch + tx] = sc[0];
-          if (BWD) dots[ty * pitch + tx] = back[0];
-        }
-        __syncthreads();
-        for (int k = threadIdx.x / R; k < span; k += kThr / R) {
-          float s = 0.f, d = 0.f;
-          for (int y = threadIdx.x % R; y < TY; y += R) {
-            s += sums[y * pitch + k];
-            if (BWD) d += dots[y * pitch + k];
-          }
-          for (int off = R / 2; off >= 1; off >>= 1) {
-            s += __shfl_xor_sync(kFull, s, off);
-            if (BWD) d += __shfl_xor_sync(kFull, d, off);
-          }
-          if (threadIdx.x % R == 0) {
-            const float r = inv_rms(p, s);
-            res[k] = r;
-            if (BWD) res2[k] = r * r * d * p.inv_D;
-          }
-        }
-        __syncthreads();  // the sums are read; the next head's go in after the next barrier of this kind
-#pragma unroll
-        for (int e = 0; e < TV; e++) {
-          sc[e] = res[tx * TV + e];
-          if (BWD) back[e] = res2[tx * TV + e];
-        }
+        __syncwarp();
       }
-#pragma unroll
-      for (int n = 0; n < NS; n++) {
-        const int unit = ty + n * TY;
-        if (unit < n_units) {
-          const Unit u = unit_of(p, unit);
-          const bool two = u.o2 < p.D;
-          if (NS > 1 || !p.norm) fetch(u, unit);  // with one pair it is still here
-          const float wa = w ? w[u.o1] : 1.f, wc = w && two ? w[u.o2] : 1.f;
+      // pass 2
+      const int rounds = (n_units + 7) / 8;
+      for (int n = 0; n < rounds; n++) {
+        const int unit = pl + 8 * n;
+        const Unit u = unit_of(p, unit);
+        const int m1 = u.on ? m : 0, m2 = u.on && u.o2 < p.D ? m : 0;
+        if (!ONE && u.on) angles(unit, u.rot);
+#pragma unroll 1
+        for (int k = 0; k < nh; k++) {
+          const int sd = h0 + k >= p.H[0], h = h0 + k - (sd ? p.H[0] : 0);
+          const QkTensor &in = p.in[sd], &out = p.out[sd];
+          const int64_t at = b * in.sb + h * in.sh + t0, oat = b * out.sb + h * out.sh + t0;
+          const float *w = p.w[sd];
+          const float wa = w && u.on ? w[u.o1] : 1.f, wc = w && m2 ? w[u.o2] : 1.f;
+          float sc[8], back[8];
+          if (p.norm) {
+            factor(k, sc);
+            if (BWD) factor(2 + k, back);
+          }
+          float a[8], c[8];
+          if (!BWD || p.norm) {
+            get_run(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m1, vec, a);
+            get_run(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, m2, vec, c);
+          }
           if (BWD) {
-            if (p.norm) {
-              float x = 0.f, y = 0.f;
+            const QkTensor &dout = p.dout[sd];
+            const int64_t dat = b * dout.sb + h * dout.sh + t0;
+            float ga[8], gc[8];
+            get_run(dout.p, dout.bf16, dat + u.o1 * dout.sr, m1, vec, ga);
+            get_run(dout.p, dout.bf16, dat + u.o2 * dout.sr, m2, vec, gc);
+            float dx = 0.f, dy = 0.f;
 #pragma unroll
-              for (int e = 0; e < TV; e++) {
-                if (e < m) {  // a step that is none has no 1 / sqrt(0) either
-                  x = fmaf(ga[e] * sc[e], a[e], x);
-                  y = fmaf(gc[e] * sc[e], c[e], y);
+            for (int e = 0; e < 8; e++) {
+              const float x = ga[e] * cs[e] + gc[e] * sn[e], y = gc[e] * cs[e] - ga[e] * sn[e];
+              ga[e] = x;
+              gc[e] = y;
+              if (p.norm) {
+                if (e < m1) {  // a step that is none has no 1 / sqrt(0) either
+                  dx = fmaf(x * sc[e], a[e], dx);
+                  dy = fmaf(y * sc[e], c[e], dy);
                 }
-                ga[e] = sc[e] * (ga[e] * wa - a[e] * back[e]);
-                gc[e] = sc[e] * (gc[e] * wc - c[e] * back[e]);
+                ga[e] = sc[e] * (x * wa - a[e] * back[e]);
+                gc[e] = sc[e] * (y * wc - c[e] * back[e]);
               }
-              dw[0][n][0] += sd ? 0.f : x;
-              dw[0][n][1] += sd ? 0.f : y;
-              dw[1][n][0] += sd ? x : 0.f;
-              dw[1][n][1] += sd ? y : 0.f;
+            }
+            if (sums) {  // over the 4 lanes of a pair; the first of them owns its place
+              dx += __shfl_xor_sync(kFull, dx, 1);
+              dy += __shfl_xor_sync(kFull, dy, 1);
+              dx += __shfl_xor_sync(kFull, dx, 2);
+              dy += __shfl_xor_sync(kFull, dy, 2);
+              if (tl == 0 && u.on) {
+                mine[sd * p.D + u.o1] += dx;
+                if (u.o2 < p.D) mine[sd * p.D + u.o2] += dy;
+              }
             }
             if (out.p) {
-              put_run<TV>(out.p, out.bf16, oat + u.o1 * out.sr, m, ga);
-              if (two) put_run<TV>(out.p, out.bf16, oat + u.o2 * out.sr, m, gc);
+              put_run(out.p, out.bf16, oat + u.o1 * out.sr, m1, vec, ga);
+              put_run(out.p, out.bf16, oat + u.o2 * out.sr, m2, vec, gc);
             }
           } else {
-            if (NS > 1) angles(u, unit);
 #pragma unroll
-            for (int e = 0; e < TV; e++) {
+            for (int e = 0; e < 8; e++) {
               const float x = p.norm ? a[e] * (sc[e] * wa) : a[e], y = p.norm ? c[e] * (sc[e] * wc) : c[e];
               a[e] = x * cs[e] - y * sn[e];
               c[e] = y * cs[e] + x * sn[e];
             }
-            put_run<TV>(out.p, out.bf16, oat + u.o1 * out.sr, m, a);
-            if (two) put_run<TV>(out.p, out.bf16, oat + u.o2 * out.sr, m, c);
+            put_run(out.p, out.bf16, oat + u.o1 * out.sr, m1, vec, a);
+            put_run(out.p, out.bf16, oat + u.o2 * out.sr, m2, vec, c);
           }
         }
       }
     }
   }
-  if (!BWD || (!p.dw[0] && !p.dw[1])) return;
-  // the block's shares of dw, rows 2 block + side: over the TX threads of a pair
-  const int lanes = TX < 32 ? TX : 32;
+  if (!sums) return;
+  __syncthreads();  // the block's shares, rows 2 block + side: the warps' in their order
+  for (int j = threadIdx.x; j < 2 * p.D; j += kThr) {
+    float t = 0.f;
+    for (int w = 0; w < kThr / 32; w++) t += sdw[w * 2 * p.D + j];
+    p.part[2 * (int64_t)blockIdx.x * p.D + j] = t;
+  }
+}
+
+// The same for heads of up to 64 elements in 16-byte runs: the runs of the heads ahead travel in a ring of cp.async slots that
+// every lane fills and reads alone, both passes read them there, and with up to 16 elements (NP = 1) or 32 (NP = 2) a lane keeps
+// its NP pairs' cosines and sines for all heads of its steps.
+template <typename T, typename Td, bool BWD, int NP> struct TimeRing {
+  static constexpr int kV = sizeof(T) / 2, kG = BWD ? sizeof(Td) / 2 : 0;  // 16-byte slots of a run of 8
+  static constexpr int kSlots = 2 * NP * (kV + kG), kStageBytes = kSlots * 512;  // of a lane; of a warp
+  static constexpr int S = kStageBytes <= 3072 ? 4 : kStageBytes <= 4096 ? 3 : 2;
+  static constexpr int kBytes = kThr / 32 * S * kStageBytes;
+};
+template <typename T, typename Td, bool BWD, int NP>
+__global__ void __launch_bounds__(kThr, BWD || NP == 2 ? 2 : 3)
+qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, int64_t items) {
+  constexpr bool PRECISE = sizeof(T) == 4;
+  using Ring = TimeRing<T, Td, BWD, NP>;
+  constexpr int S = Ring::S, kV = Ring::kV, kG = Ring::kG;
+  extern __shared__ __align__(16) char smem[];  // the ring, then (warps, 2, D) sums of dw
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane & 3, pl = lane >> 2;
+  const int all = p.H[0] + p.H[1];
+  const bool sums = BWD && p.norm && (p.dw[0] || p.dw[1]), reads_v = !BWD || p.norm;
+  float *const sdw = reinterpret_cast<float *>(smem + Ring::kBytes), *const mine = sdw + warp * 2 * p.D;
+  if (sums) {
+    for (int j = threadIdx.x; j < kThr / 32 * 2 * p.D; j += kThr) sdw[j] = 0.f;
+    __syncthreads();
+  }
+  __shared__ double positions[kThr / 32][32];
+  __shared__ __align__(16) float factors[kThr / 32][BWD ? 2 : 1][32];
+  char *const base = smem + warp * S * Ring::kStageBytes + lane * 16;
+  auto slot = [&](int stage, int k) { return base + (stage * Ring::kSlots + k) * 512; };
+  Unit u[NP];
 #pragma unroll
-  for (int sd = 0; sd < 2; sd++) {
-    if (!p.dw[sd]) continue;
+  for (int n = 0; n < NP; n++) u[n] = unit_of(p, pl + 8 * n);
 #pragma unroll
-    for (int n = 0; n < NS; n++) {
-      float x = dw[sd][n][0], y = dw[sd][n][1];
-      for (int off = lanes / 2; off >= 1; off >>= 1) {
-        x += __shfl_xor_sync(kFull, x, off);
-        y += __shfl_xor_sync(kFull, y, off);
-      }
-      if (TX > 32) {
-        __syncthreads();
-        if (threadIdx.x % 32 == 0) {
-          sh[threadIdx.x / 16] = x;
-          sh[threadIdx.x / 16 + 1] = y;
+  for (int k = 0; k < S * Ring::kSlots; k++) *reinterpret_cast<uint4 *>(slot(0, k)) = make_uint4(0, 0, 0, 0);
+  const int own = 8 * tl + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);  // the step whose sum this lane ends with
+  // one head of one item at a time
+  struct Job {
+    int64_t item, b, t0;  // t0: of the warp
+    int h, h_end;
+    bool on;
+  };
+  const int64_t per_row = (p.L + 31) / 32, stride = (int64_t)gridDim.x * (kThr / 32);
+  auto open = [&](Job &j) {
+    j.on = j.item < items;
+    if (!j.on) return;
+    int64_t bc, tt, chunk;
+    divide(j.item, per_row, bc, tt);
+    divide(bc, chunks, j.b, chunk);
+    j.t0 = tt * 32;
+    j.h = (int)chunk * heads;
+    j.h_end = min(all, j.h + heads);
+  };
+  auto next = [&](Job &j) {
+    if (++j.h == j.h_end) {
+      j.item += stride;
+      open(j);
+      return true;
+    }
+    return false;
+  };
+  Job ahead;
+  ahead.item = (int64_t)blockIdx.x * (kThr / 32) + warp;
+  open(ahead);
+  Job now = ahead;
+  // 8 steps of one row into the slots from k on, element by element where not all of them live
+  auto copy = [&](int stage, int k, const auto *src, int m) {
+    using E = std::remove_cv_t<std::remove_reference_t<decltype(*src)>>;
+    if (m == 8) {
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(E) / 2; j++) cp_async16(slot(stage, k + j), reinterpret_cast<const char *>(src) + 16 * j);
+    } else {
+      Raw8<E> r;
+      zero8(r);
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        if (e < m) put8(r, e, src[e]);
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(E) / 2; j++) *reinterpret_cast<uint4 *>(slot(stage, k + j)) = reinterpret_cast<const uint4 *>(&r)[j];
+    }
+  };
+  auto live = [&](const Job &j) {
+    const int64_t left = p.L - j.t0 - 8 * tl;
+    return (int)(left < 0 ? 0 : left < 8 ? left : 8);
+  };
+  auto fetch = [&](int stage) {
+    if (ahead.on) {
+      const int m = live(ahead), sd = ahead.h >= p.H[0], h = ahead.h - (sd ? p.H[0] : 0);
+      const int64_t t = ahead.t0 + 8 * tl;
+#pragma unroll
+      for (int n = 0; n < NP; n++) {
+        if (!u[n].on) continue;
+        const bool two = u[n].o2 < p.D;
+        if (reads_v) {
+          const QkTensor &x = p.in[sd];
+          const T *a = static_cast<const T *>(x.p) + ahead.b * x.sb + h * x.sh + t;
+          copy(stage, 2 * n * kV, a + u[n].o1 * x.sr, m);
+          if (two) copy(stage, (2 * n + 1) * kV, a + u[n].o2 * x.sr, m);
         }
-        __syncthreads();
-        x = y = 0.f;
-        for (int k = 0; k < TX / 32; k++) {
-          x += sh[2 * (ty * (TX / 32) + k)];
-          y += sh[2 * (ty * (TX / 32) + k) + 1];
+        if (BWD) {
+          const QkTensor &x = p.dout[sd];
+          const Td *a = static_cast<const Td *>(x.p) + ahead.b * x.sb + h * x.sh + t;
+          copy(stage, 2 * NP * kV + 2 * n * kG, a + u[n].o1 * x.sr, m);
+          if (two) copy(stage, 2 * NP * kV + (2 * n + 1) * kG, a + u[n].o2 * x.sr, m);
         }
       }
-      const int unit = ty + n * TY;
-      if (tx == 0 && unit < n_units) {
-        const Unit u = unit_of(p, unit);
-        float *row = p.part + (2 * (int64_t)blockIdx.x + sd) * p.D;
-        row[u.o1] = x;
-        if (u.o2 < p.D) row[u.o2] = y;
+      next(ahead);
+    }
+    cp_async_commit();
+  };
+  auto take = [&](int stage, int k, auto tag, float *v) {
+    Raw8<decltype(tag)> r;
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(tag) / 2; j++) reinterpret_cast<uint4 *>(&r)[j] = *reinterpret_cast<const uint4 *>(slot(stage, k + j));
+    unpack8(r, v);
+  };
+#pragma unroll
+  for (int j = 0; j < S - 1; j++) fetch(j);
+  constexpr int kKeep = NP <= 2 ? NP : 1;  // pairs whose angles are kept
+  float cs[kKeep][8], sn[kKeep][8];
+  auto angles = [&](int n, int at) {
+    const double f = u[n].on && u[n].rot ? frequency(p, pl + 8 * n) : 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      cs[at][e] = 1.f;
+      sn[at][e] = 0.f;
+      if (u[n].on && u[n].rot) turn<PRECISE>(positions[warp][8 * tl + e], f, p.rot_scale, cs[at][e], sn[at][e]);
+    }
+  };
+  int stage = 0;
+  bool fresh = true;
+  while (now.on) {
+    fetch(stage == 0 ? S - 1 : stage - 1);
+    const int m = live(now), sd = now.h >= p.H[0], h = now.h - (sd ? p.H[0] : 0);
+    if (fresh) {
+      __syncwarp();  // the item before is done with the positions
+      const int64_t t = now.t0 + lane;
+      positions[warp][lane] = p.rot && t < p.L ? position(p, now.b * p.L + t, t) : 0.0;
+      __syncwarp();
+      if (NP <= 2) {
+#pragma unroll
+        for (int n = 0; n < kKeep; n++) angles(n, n);
       }
     }
+    cp_async_wait<S - 1>();
+    const float *w = p.w[sd];
+    float sc[8], back[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) sc[e] = back[e] = 0.f;
+    if (p.norm) {
+#pragma unroll
+      for (int n = 0; n < NP; n++) {
+        float a[8], c[8];
+        take(stage, 2 * n * kV, T(), a);
+        take(stage, (2 * n + 1) * kV, T(), c);
+#pragma unroll
+        for (int e = 0; e < 8; e++) sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
+        if constexpr (BWD) {
+          constexpr bool keep = NP <= 2;
+          if (!keep) angles(n, 0);
+          const int at = keep ? n : 0;
+          const float wa = w && u[n].on ? w[u[n].o1] : 1.f, wc = w && u[n].on && u[n].o2 < p.D ? w[u[n].o2] : 1.f;
+          float ga[8], gc[8];
+          take(stage, 2 * NP * kV + 2 * n * kG, Td(), ga);
+          take(stage, 2 * NP * kV + (2 * n + 1) * kG, Td(), gc);
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const float x = ga[e] * cs[at][e] + gc[e] * sn[at][e], y = gc[e] * cs[at][e] - ga[e] * sn[at][e];
+            back[e] = fmaf(x * wa, a[e], fmaf(y * wc, c[e], back[e]));
+          }
+        }
+      }
+      const float r = inv_rms(p, scatter_sum(lane, sc));
+      const float q = BWD ? r * r * scatter_sum(lane, back) * p.inv_D : 0.f;
+      __syncwarp();  // the head before is done with the factors
+      factors[warp][0][own] = r;
+      if (BWD) factors[warp][BWD ? 1 : 0][own] = q;
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        sc[e] = factors[warp][0][8 * tl + e];
+        if (BWD) back[e] = factors[warp][BWD ? 1 : 0][8 * tl + e];
+      }
+    }
+    const QkTensor &out = p.out[sd];
+    const int64_t to = now.b * out.sb + h * out.sh + now.t0 + 8 * tl;
+#pragma unroll
+    for (int n = 0; n < NP; n++) {
+      const bool two = u[n].on && u[n].o2 < p.D;
+      constexpr bool keep = NP <= 2;
+      if (!keep) angles(n, 0);
+      const int at = keep ? n : 0;
+      const float wa = w && u[n].on ? w[u[n].o1] : 1.f, wc = w && two ? w[u[n].o2] : 1.f;
+      float a[8], c[8];
+      if (reads_v) {
+        take(stage, 2 * n * kV, T(), a);
+        take(stage, (2 * n + 1) * kV, T(), c);
+      }
+      if constexpr (BWD) {
+        float ga[8], gc[8], dx = 0.f, dy = 0.f;
+        take(stage, 2 * NP * kV + 2 * n * kG, Td(), ga);
+        take(stage, 2 * NP * kV + (2 * n + 1) * kG, Td(), gc);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float x = ga[e] * cs[at][e] + gc[e] * sn[at][e], y = gc[e] * cs[at][e] - ga[e] * sn[at][e];
+          ga[e] = x;
+          gc[e] = y;
+          if (p.norm) {
+            if (e < m) {  // a step that is none has no 1 / sqrt(0) either
+              dx = fmaf(x * sc[e], a[e], dx);
+              dy = fmaf(y * sc[e], c[e], dy);
+            }
+            ga[e] = sc[e] * (x * wa - a[e] * back[e]);
+            gc[e] = sc[e] * (y * wc - c[e] * back[e]);
+          }
+        }
+        if (sums) {  // over the 4 lanes of a pair; the first of them owns its place
+          dx += __shfl_xor_sync(kFull, dx, 1);
+          dy += __shfl_xor_sync(kFull, dy, 1);
+          dx += __shfl_xor_sync(kFull, dx, 2);
+          dy += __shfl_xor_sync(kFull, dy, 2);
+          if (tl == 0 && u[n].on) {
+            mine[sd * p.D + u[n].o1] += dx;
+            if (two) mine[sd * p.D + u[n].o2] += dy;
+          }
+        }
+        if (out.p) {
+          if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, 1, ga);
+          if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, 1, gc);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float x = p.norm ? a[e] * (sc[e] * wa) : a[e], y = p.norm ? c[e] * (sc[e] * wc) : c[e];
+          a[e] = x * cs[at][e] - y * sn[at][e];
+          c[e] = y * cs[at][e] + x * sn[at][e];
+        }
+        if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, 1, a);
+        if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, 1, c);
+      }
+    }
+    stage = stage == S - 1 ? 0 : stage + 1;
+    fresh = next(now);
+  }
+  if (!sums) return;
+  __syncthreads();  // the block's shares, rows 2 block + side: the warps' in their order
+  for (int j = threadIdx.x; j < 2 * p.D; j += kThr) {
+    float t = 0.f;
+    for (int w = 0; w < kThr / 32; w++) t += sdw[w * 2 * p.D + j];
+    p.part[2 * (int64_t)blockIdx.x * p.D + j] = t;
   }
 }
 
@@ -835,33 +1125,34 @@ int pow2_at_least(int n) {
 // Pair units of a row.
 int pairs_of(const QkParams &p) { return p.rot / 2 + (p.D - p.rot + 1) / 2; }
 
-// Lanes that hold a row: a unit of 16 elements each (vec); at least a fourth of the pairs otherwise, at most a warp.
-int lanes_per_row(const QkParams &p) {
-  if (p.vec) return pow2_at_least(p.D / 16);
-  const int g = pow2_at_least((pairs_of(p) + 3) / 4);
-  return g < 32 ? g : 32;
+// The most elements (8, 4, 2; 1 of fp32) that every run of a row starts at multiples of, and the strides and addresses of both
+// sides are; 0 where a row does not make such runs or more units than a warp has lanes.
+int run_of(const QkParams &p) {
+  const int units = p.interleaved ? (p.D + 15) / 16 : (p.rot / 2 + 7) / 8 + (p.D - p.rot + 15) / 16;
+  if (units > 32) return 0;
+  bool wide = true;  // fp32 throughout: single elements travel as 4 bytes
+  for (int s = 0; s < 2; s++)
+    if (p.H[s])
+      for (const QkTensor *t : {&p.in[s], &p.dout[s]})
+        if (t->bf16) wide = false;  // (of a tensor that is not read too: the kernel's type goes by it)
+  for (int V = 8; V >= (wide ? 1 : 2); V /= 2) {
+    bool fits = p.D % V == 0 && (p.interleaved || (p.rot / 2 % V == 0 && p.rot % V == 0));
+    for (int s = 0; s < 2 && fits; s++) {
+      if (p.H[s] == 0) continue;
+      for (const QkTensor *t : {&p.in[s], &p.out[s], &p.dout[s]}) {
+        const int bytes = V * (t->bf16 ? 2 : 4) < 16 ? V * (t->bf16 ? 2 : 4) : 16;
+        if (t->p && (reinterpret_cast<uintptr_t>(t->p) % bytes || t->sb % V || t->sh % V || t->sr % V)) fits = false;
+      }
+    }
+    if (fits) return V;
+  }
+  return 0;
 }
-
-// Time innermost: threads over time, heads per tile, tiles, shared memory. As few pairs a thread as possible with 8
-// threads (of 8 steps) or 32 (of one step) over time at least, so that a row's accesses are 64 bytes and more; all heads of
-// a batch element in one tile, for their common angles, where that leaves two tiles per SM.
-struct TimePlan {
-  int TX, heads;
-  int64_t chunks, tiles;
-  int smem;
-};
-TimePlan time_plan(const QkParams &p, bool bwd) {
-  TimePlan t;
-  const int TV = p.vec ? 8 : 1, ty = pow2_at_least(pairs_of(p)), most = p.vec ? 32 : 8;
-  t.TX = kThr / (ty < most ? ty : most);
-  const int span = t.TX * TV, R = span < kThr ? kThr / span : 1;
-  const int64_t slices = p.Bt * ((p.L + span - 1) / span);
-  const int all = p.H[0] + p.H[1];
-  t.heads = slices >= 2 * 148 ? all : 1;
-  t.chunks = (all + t.heads - 1) / t.heads;
-  t.tiles = slices * t.chunks;
-  t.smem = (int)sizeof(float) * ((bwd ? 2 : 1) * (kThr / t.TX) * (span + 32 / R) + 2 * span);
-  return t;
+// Lanes that hold a row: a unit each, or four pairs (eight of the largest heads).
+int lanes_per_row(const QkParams &p, int V) {
+  const int pairs = pairs_of(p), per = pairs <= 128 ? 4 : 8;
+  if (!V) return pow2_at_least((pairs + per - 1) / per);
+  return pow2_at_least(p.interleaved ? (p.D + 15) / 16 : (p.rot / 2 + 7) / 8 + (p.D - p.rot + 15) / 16);
 }
 
 // At most `most` CTAs over both sides, in proportion to their work (in CTAs), at least one where a side has any.
@@ -879,12 +1170,13 @@ void split_blocks(const int64_t *work, int64_t most, int *nb0, int *nb1) {
 
 // How the rows of both sides are cut: CTAs of the queries and of both, rows per warp (whole steps of 32 / G rows).
 struct RowPlan {
-  int G, nb0, nb;
+  int V, G, nb0, nb;
   int64_t per[2];
 };
 bool plan_rows(const QkParams &p, int64_t most, RowPlan *r) {
   constexpr int kWarps = kThr / 32;
-  r->G = lanes_per_row(p);
+  r->V = run_of(p);
+  r->G = lanes_per_row(p, r->V);
   const int step = 32 / r->G;
   int64_t rows[2], work[2];
   int n[2];
@@ -914,36 +1206,58 @@ template <typename K> cudaError_t launch_rows(K kernel, const QkParams &p, const
   return cudaGetLastError();
 }
 
-// Head elements innermost, forward (Td = T) or backward. CTAs: what fits the SMs at once, at most kBwdCtas of a backward.
+// Head elements innermost, forward (Td = T) or backward. CTAs: what fits the SMs at once.
 template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams &p, RowPlan *r, cudaStream_t s) {
-  if (!plan_rows(p, BWD ? (p.vec ? 148 * 2 : kBwdCtas) : 148 * (p.vec ? 3 : 6), r)) return cudaErrorInvalidConfiguration;
+  if (!plan_rows(p, BWD ? kBwdCtas : 3 * 148, r)) return cudaErrorInvalidConfiguration;
   const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * (kThr / r->G) * p.D : 0;
-  if (p.vec) {
-    constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
-    const int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>;
-    return launch_rows(p.interleaved ? qk_rows_kernel<T, Td, BWD, true> : qk_rows_kernel<T, Td, BWD, false>, p, *r,
-                       sums > ring ? sums : ring, s);
+  constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
+  constexpr int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>;
+  const int smem = sums > ring ? sums : ring;
+  const bool inter = p.interleaved;
+  switch (r->V) {
+    case 8: return launch_rows(inter ? qk_rows_kernel<T, Td, BWD, true, 8> : qk_rows_kernel<T, Td, BWD, false, 8>, p, *r, smem, s);
+    case 4: return launch_rows(inter ? qk_rows_kernel<T, Td, BWD, true, 4> : qk_rows_kernel<T, Td, BWD, false, 4>, p, *r, smem, s);
+    case 2: return launch_rows(inter ? qk_rows_kernel<T, Td, BWD, true, 2> : qk_rows_kernel<T, Td, BWD, false, 2>, p, *r, smem, s);
+    case 1:
+      if constexpr (sizeof(T) == 4 && sizeof(Td) == 4)
+        return launch_rows(inter ? qk_rows_kernel<T, Td, BWD, true, 1> : qk_rows_kernel<T, Td, BWD, false, 1>, p, *r, smem, s);
   }
-  return launch_rows(pairs_of(p) <= 4 * r->G ? qk_pairs_kernel<T, Td, BWD, 4> : qk_pairs_kernel<T, Td, BWD, 8>, p, *r, sums, s);
+  return launch_rows(pairs_of(p) <= 128 ? qk_pairs_kernel<T, Td, BWD, 4> : qk_pairs_kernel<T, Td, BWD, 8>, p, *r, sums, s);
 }
 
-// CTAs of a time_last launch: four per SM forwards, the backward's two (each keeps a share of dw of both sides).
-template <typename T, bool BWD> cudaError_t time_run(const QkParams &p, int *nb, cudaStream_t s) {
-  const TimePlan t = time_plan(p, BWD);
-  const int64_t most = BWD ? 2 * 148 : 4 * 148;
-  *nb = (int)(t.tiles < most ? t.tiles : most);
-  const int pairs = pairs_of(p), TY = kThr / t.TX;
-  const auto kernel = p.vec ? (pairs <= TY ? qk_time_kernel<T, 8, 1, BWD> : qk_time_kernel<T, 8, 8, BWD>)
-                            : (pairs <= TY       ? qk_time_kernel<T, 1, 1, BWD>
-                               : pairs <= 4 * TY ? qk_time_kernel<T, 1, 4, BWD>
-                                                 : qk_time_kernel<T, 1, 32, BWD>);
-  kernel<<<*nb, kThr, t.smem, s>>>(p, t.TX, t.heads, t.chunks, t.tiles);
+// Time innermost. All heads of a batch element go to one warp, for their common angles, where that leaves 16 warps per SM. CTAs:
+// what fits the SMs at once (the backward's each keep a share of dw of both sides).
+template <typename T, typename Td, bool BWD, int NP>
+cudaError_t time_ring(const QkParams &p, int nb, int heads, int64_t chunks, int64_t items, int sums, cudaStream_t s) {
+  const auto kernel = qk_time_ring_kernel<T, Td, BWD, NP>;
+  const int smem = TimeRing<T, Td, BWD, NP>::kBytes + sums;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<nb, kThr, smem, s>>>(p, heads, chunks, items);
+  return cudaGetLastError();
+}
+
+template <typename T, typename Td, bool BWD> cudaError_t time_run(const QkParams &p, int *nb, cudaStream_t s) {
+  const int64_t slices = p.Bt * ((p.L + 31) / 32);
+  const int all = p.H[0] + p.H[1], pairs = pairs_of(p);
+  const int heads = slices >= 16 * 148 ? all : slices * 2 >= 16 * 148 && all > 2 ? 2 : 1;
+  const int64_t chunks = (all + heads - 1) / heads, items = slices * chunks, ctas = (items + kThr / 32 - 1) / (kThr / 32);
+  const int64_t most = BWD ? kBwdCtas : 3 * 148;
+  *nb = (int)(ctas < most ? ctas : most);
+  const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * kThr / 32 * 2 * p.D : 0;
+  if (p.vec && pairs <= 8) return time_ring<T, Td, BWD, 1>(p, *nb, heads, chunks, items, sums, s);
+  if (p.vec && pairs <= 16) return time_ring<T, Td, BWD, 2>(p, *nb, heads, chunks, items, sums, s);
+  // four pairs a lane: where the ring leaves room for two CTAs per SM
+  if constexpr (TimeRing<T, Td, BWD, 4>::kBytes <= 100 * 1024)
+    if (p.vec && pairs <= 32) return time_ring<T, Td, BWD, 4>(p, *nb, heads, chunks, items, sums, s);
+  const auto kernel = pairs <= 8 ? qk_time_kernel<T, BWD, true> : qk_time_kernel<T, BWD, false>;
+  kernel<<<*nb, kThr, sums, s>>>(p, heads, chunks, items);
   return cudaGetLastError();
 }
 
 template <typename T> cudaError_t fwd_t(const QkParams &p, cudaStream_t s) {
   int nb;
-  if (p.time_last) return time_run<T, false>(p, &nb, s);
+  if (p.time_last) return time_run<T, T, false>(p, &nb, s);
   RowPlan r;
   return rows_run<T, T, false>(p, &r, s);
 }
@@ -953,7 +1267,7 @@ template <typename T> cudaError_t bwd_t(const QkParams &p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.D + 31) / 32), 2);
   if (p.time_last) {
     int nb;
-    const cudaError_t e = time_run<T, true>(p, &nb, s);
+    const cudaError_t e = p.dout[p.H[0] == 0].bf16 ? time_run<T, __nv_bfloat16, true>(p, &nb, s) : time_run<T, float, true>(p, &nb, s);
     if (e != cudaSuccess || !sums) return e;
     qk_dw_kernel<<<grid, 1024, 0, s>>>(p, nb, 1, nb, 2);
   } else {
@@ -967,12 +1281,11 @@ template <typename T> cudaError_t bwd_t(const QkParams &p, cudaStream_t s) {
 
 }  // namespace
 
-// Whatever the plan: at most kBwdCtas shares, one more where a side rounds up from none; two from each of 2 * 148 CTAs with
-// time innermost.
+// Whatever the plan: at most kBwdCtas shares, one more where a side rounds up from none; two from each of kBwdCtas CTAs with
+// time innermost. (qk_dw_kernel reads up to kBwdCtas + 32 - kBwdCtas % 32 of a side.)
 size_t qk_bwd_workspace_bytes(const QkParams &p) {
-  return p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(4 * 148) * (size_t)p.D : 0;
+  return p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(2 * kBwdCtas + 2) * (size_t)p.D : 0;
 }
-static_assert(kBwdCtas + 2 <= 4 * 148 && 2 * 148 <= kBwdCtas, "the workspace and the reduction hold every plan's shares");
 
 cudaError_t launch_qk_fwd(const QkParams &p, int in_bf16, cudaStream_t s) {
   return in_bf16 ? fwd_t<__nv_bfloat16>(p, s) : fwd_t<float>(p, s);
