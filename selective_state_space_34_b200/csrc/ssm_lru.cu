@@ -658,6 +658,188 @@ __global__ void __launch_bounds__(32 * W, W <= 4 ? 16 / W : 1) lru_bwd_kernel(co
   if (q.p_di) q.p_di[row] = si;
 }
 
+// ---- rows of up to 128 places ------------------------------------------------------------------
+
+// G lanes a row (G a power of two, G * 8 places and more of them), 32 / G rows a warp, one group of 8 steps a lane:
+// the same composition over G lanes instead of 32, without rounds. (A warp per row would leave lanes idle and be bound by the rate at
+// which CTAs start: 8 x 5000 rows of 8 or 100 steps took 33 us forwards whatever their length.)
+template <bool CUT> __device__ __forceinline__ void scan_up_group(int gl, int G, float &P, float &H) {
+  for (int off = 1; off < G; off <<= 1) {
+    const float Q = __shfl_up_sync(kFull, P, off), A = __shfl_up_sync(kFull, H, off);
+    if (gl >= off) {
+      H = after<CUT>(P, A, H);
+      P = times<CUT>(P, Q);
+    }
+  }
+}
+template <bool CUT> __device__ __forceinline__ void scan_down_group(int gl, int G, float &S, float &M) {
+  for (int off = 1; off < G; off <<= 1) {
+    const float Z = __shfl_down_sync(kFull, S, off), N = __shfl_down_sync(kFull, M, off);
+    if (gl + off < G) {
+      M = after<CUT>(S, N, M);
+      S = times<CUT>(S, Z);
+    }
+  }
+}
+
+template <typename T, typename Tout, bool RESET>
+__global__ void __launch_bounds__(128) lru_fwd_short_kernel(const __grid_constant__ LruParams p, int G) {
+  const int64_t rows = p.Bt * p.Dn, id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / G;
+  const int gl = threadIdx.x & (G - 1);
+  const bool live = id < rows;
+  const int64_t row = live ? id : rows - 1;  // groups behind the last row follow along on it and store nothing
+  const int64_t b = row / p.Dn, d = row - b * p.Dn;
+  const Row R = row_of(p, row, b);
+  const int64_t total = rows * p.L;
+  const int t0 = 8 * gl - R.f, L = (int)p.L;
+  Raw8<T> rx, rr, ri;
+  load_edge(static_cast<const T *>(p.x), R, t0, total, p.vec, rx);
+  load_edge(static_cast<const T *>(p.r), R, t0, total, p.vec, rr);
+  load_edge(static_cast<const T *>(p.i), R, t0, total, p.vec, ri);
+  const uint64_t cut = RESET ? load_resets(p, b, R, t0) : 0;
+  const Gate gr = gate_of(p.r_bias ? p.r_bias[d] : 0.f), gi = gate_of(p.i_bias ? p.i_bias[d] : 0.f);
+  const float rate = decay_rate(p.c, p.lam[d]), h0 = p.h0 ? p.h0[row] : 0.f;
+  float2 a[4], bb[4], r[4], g[4];
+  arguments(rr, gr, r);
+  arguments(ri, gi, g);
+  pairs(rx, bb);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    float2 ev, sq, is;
+    sigmoid2(r[j], g[j], r[j], g[j], ev);
+    decay<false>(fma2(r[j], splat(rate), splat(kTiny)), a[j], sq, is);
+    bb[j] = mul2(mul2(mul2(sq, is), g[j]), bb[j]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    if (t0 + e < 0 || t0 + e >= R.len) elem(a, e) = 1.f, elem(bb, e) = 0.f;
+    if (RESET && (cut >> (8 * e) & 0xff)) elem(a, e) = 0.f;
+  }
+  float2 P2, H2;
+  compose<RESET>(a, bb, P2, H2);
+  float P = times<RESET>(P2.y, P2.x), H = after<RESET>(P2.y, H2.x, H2.y);
+  scan_up_group<RESET>(gl, G, P, H);
+  const float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
+  float2 h;
+  h.x = gl == 0 ? h0 : after<RESET>(Pe, h0, He);
+  h.y = after<RESET>(P2.x, h.x, H2.x);
+#pragma unroll
+  for (int j = 0; j < 4; j++) bb[j] = h = after2<RESET>(a[j], h, bb[j]);
+  if (!live) return;
+  if (p.states && gl == 0) p.states[row * p.n_states] = h0;
+  if (p.h_last && gl == G - 1) p.h_last[row] = h.y;
+  if (p.out) {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (t0 + e >= R.len) elem(bb, e) = 0.f;
+    store_group(static_cast<Tout *>(p.out), R, false, t0, L, p.vec_out, bb);
+  }
+}
+
+template <typename T, typename Tg, bool RESET>
+__global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constant__ LruBwdParams q, int G) {
+  const LruParams &p = q.f;
+  const int64_t rows = p.Bt * p.Dn, id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / G;
+  const int gl = threadIdx.x & (G - 1);
+  const bool live = id < rows;
+  const int64_t row = live ? id : rows - 1;
+  const int64_t b = row / p.Dn, d = row - b * p.Dn;
+  const Row R = row_of(p, row, b);
+  const int64_t total = rows * p.L;
+  const int t0 = 8 * gl - R.f, L = (int)p.L;
+  Raw8<T> rx, rr, ri, rd;
+  load_edge(static_cast<const T *>(p.x), R, t0, total, p.vec, rx);
+  load_edge(static_cast<const T *>(p.r), R, t0, total, p.vec, rr);
+  load_edge(static_cast<const T *>(p.i), R, t0, total, p.vec, ri);
+  load_edge(static_cast<const T *>(q.dout), R, t0, total, p.vec, rd);
+  const uint64_t cut = RESET ? load_resets(p, b, R, t0) : 0;
+  const Gate gr = gate_of(p.r_bias ? p.r_bias[d] : 0.f), gi = gate_of(p.i_bias ? p.i_bias[d] : 0.f);
+  const float lam = p.lam[d];
+  const float rate = decay_rate(p.c, lam), inv_rate = rate > 0.f ? 1.f / rate : 0.f;
+  const float hin = p.states[row * p.n_states], behind = q.dh_last ? q.dh_last[row] : 0.f;
+  float2 a[4], y[4], u[4], v[4], z[4], bb[4], dv[4];
+  arguments(rr, gr, y);
+  arguments(ri, gi, v);
+  pairs(rx, bb);
+  pairs(rd, dv);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    float2 rg, g, ev, sq, is;
+    sigmoid2(y[j], v[j], rg, g, ev);
+    y[j] = fma2(rg, splat(rate), splat(kTiny));
+    decay<false>(y[j], a[j], sq, is);
+    u[j] = mul2(mul2(sq, is), g);
+    bb[j] = mul2(bb[j], u[j]);
+    v[j] = mul2(bb[j], mul2(ev, g));
+    z[j] = mul2(mul2(mul2(y[j], is), is), bb[j]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    if (t0 + e < 0 || t0 + e >= R.len) {
+      elem(a, e) = 1.f;
+      elem(bb, e) = elem(y, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+    }
+    if (RESET && (cut >> (8 * e) & 0xff)) elem(a, e) = 0.f;
+  }
+  float2 P2, H2, M2 = splat(0.f);
+  compose<RESET>(a, bb, P2, H2);
+  // a cut stops mu whatever the other factors are (NaN, in a sequence of its own)
+  const float Sx = RESET && (cut & 0xffffffffu) ? 0.f : P2.x, Sy = RESET && cut >> 32 ? 0.f : P2.y;
+#pragma unroll
+  for (int j = 3; j >= 0; j--) M2 = after2<RESET>(a[j], add2(dv[j], M2), splat(0.f));
+  float P = times<RESET>(P2.y, P2.x), H = after<RESET>(P2.y, H2.x, H2.y);
+  float S = times<RESET>(Sx, Sy), M = after<RESET>(Sx, M2.y, M2.x);
+  scan_up_group<RESET>(gl, G, P, H);
+  scan_down_group<RESET>(gl, G, S, M);
+  const float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
+  const float Se = __shfl_down_sync(kFull, S, 1), Me = __shfl_down_sync(kFull, M, 1);
+  float2 h, mu;
+  h.x = gl == 0 ? hin : after<RESET>(Pe, hin, He);
+  h.y = after<RESET>(P2.x, h.x, H2.x);
+  mu.y = gl == G - 1 ? behind : after<RESET>(Se, behind, Me);
+  mu.x = after<RESET>(Sy, mu.y, M2.y);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    h = after2<RESET>(a[j], h, bb[j]);
+    z[j] = fma2(z[j], splat(-1.f), mul2(y[j], h));  // y (h - b / s)
+  }
+#pragma unroll
+  for (int j = 3; j >= 0; j--) {
+    const float2 lm = add2(dv[j], mu);
+    mu = after2<RESET>(a[j], lm, splat(0.f));
+    u[j] = mul2(u[j], lm);
+    v[j] = mul2(v[j], lm);
+    bb[j] = mul2(z[j], lm);
+    z[j] = mul2(bb[j], fma2(y[j], splat(inv_rate), splat(-1.f)));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; e++)  // steps outside the row hold 0 (0 times an infinite lambda would not be)
+    if (t0 + e < 0 || t0 + e >= R.len) elem(u, e) = elem(v, e) = elem(z, e) = elem(bb, e) = 0.f;
+  float2 sq2 = splat(0.f), sr2 = splat(0.f), si2 = splat(0.f);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    sq2 = add2(sq2, bb[j]);
+    sr2 = add2(sr2, z[j]);
+    si2 = add2(si2, v[j]);
+  }
+  float sq = sq2.x + sq2.y, sr = sr2.x + sr2.y, si = si2.x + si2.y;
+  for (int off = G / 2; off >= 1; off >>= 1) {
+    sq += __shfl_xor_sync(kFull, sq, off);
+    sr += __shfl_xor_sync(kFull, sr, off);
+    si += __shfl_xor_sync(kFull, si, off);
+  }
+  if (!live) return;
+  if (q.dx) store_group(static_cast<Tg *>(q.dx), R, false, t0, L, q.vec_grad, u);
+  if (q.di) store_group(static_cast<Tg *>(q.di), R, false, t0, L, q.vec_grad, v);
+  if (q.dr) store_group(static_cast<Tg *>(q.dr), R, false, t0, L, q.vec_grad, z);
+  if (gl) return;
+  if (q.dh0) q.dh0[row] = mu.x;
+  const float sp = softplus<true>(lam);
+  if (q.p_dlam) q.p_dlam[row] = -sq * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
+  if (q.p_dr) q.p_dr[row] = sr;
+  if (q.p_di) q.p_di[row] = si;
+}
+
 // Per-row sums over the batch in a fixed order.
 __global__ void __launch_bounds__(128) lru_param_sum_kernel(const __grid_constant__ LruBwdParams q) {
   const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -751,6 +933,15 @@ template <typename K> cudaError_t allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// Lanes per row of the short-row kernels, 0 for longer rows.
+int short_lanes(int64_t L) {
+  const int64_t groups = (L + (L % 8 ? 7 : 0) + 7) / 8;  // rows of whole groups start on one
+  if (groups > 16) return 0;
+  int g = 1;
+  while (g < groups) g *= 2;
+  return g;
+}
+
 template <typename T, typename Tout, int W>
 cudaError_t fwd_w(const LruParams &p, cudaStream_t s) {
   const int64_t blocks = p.Bt * p.Dn;
@@ -763,6 +954,13 @@ cudaError_t fwd_w(const LruParams &p, cudaStream_t s) {
 }
 
 template <typename T, typename Tout> cudaError_t fwd_t(const LruParams &p, cudaStream_t s) {
+  if (const int G = short_lanes(p.L)) {
+    const int64_t blocks = (p.Bt * p.Dn * G + 127) / 128;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const auto kernel = p.reset ? lru_fwd_short_kernel<T, Tout, true> : lru_fwd_short_kernel<T, Tout, false>;
+    kernel<<<(unsigned)blocks, 128, 0, s>>>(p, G);
+    return cudaGetLastError();
+  }
   switch (warps_per_row(p.Bt * p.Dn, p.L)) {
     case 1: return fwd_w<T, Tout, 1>(p, s);
     case 4: return fwd_w<T, Tout, 4>(p, s);
@@ -783,6 +981,13 @@ cudaError_t bwd_w(const LruBwdParams &q, cudaStream_t s) {
 }
 
 template <typename T, typename Tg> cudaError_t bwd_t(const LruBwdParams &q, cudaStream_t s) {
+  if (const int G = short_lanes(q.f.L)) {
+    const int64_t blocks = (q.f.Bt * q.f.Dn * G + 127) / 128;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const auto kernel = q.f.reset ? lru_bwd_short_kernel<T, Tg, true> : lru_bwd_short_kernel<T, Tg, false>;
+    kernel<<<(unsigned)blocks, 128, 0, s>>>(q, G);
+    return cudaGetLastError();
+  }
   switch (warps_per_row(q.f.Bt * q.f.Dn, q.f.L)) {
     case 1: return bwd_w<T, Tg, 1>(q, s);
     case 4: return bwd_w<T, Tg, 4>(q, s);

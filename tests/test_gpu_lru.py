@@ -45,7 +45,7 @@ def compare(got, want, half, grad_half=None):
 FULL = ("r_bias", "i_bias", "h0")
 CASES = [
     # Bt, Dn, L: one token; inside a group; a group; around a chunk; rows off the 16-byte boundary
-    (1, 1, 1), (2, 3, 5), (1, 4, 8), (2, 5, 255), (1, 2, 256), (3, 3, 257), (2, 6, 513), (2, 37, 777), (1, 3, 2049),
+    (1, 1, 1), (2, 3, 5), (1, 4, 8), (3, 50, 2), (5, 7, 16), (2, 33, 57), (3, 5, 120), (2, 3, 121), (1, 3, 128), (2, 2, 129), (2, 5, 255), (1, 2, 256), (3, 3, 257), (2, 6, 513), (2, 37, 777), (1, 3, 2049),
     (1, 2, 5000), (2, 9, 1024),
 ]
 
@@ -82,10 +82,10 @@ def test_output_types_and_no_options(dtype, out_dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("Bt,Dn,L", [(3, 5, 40), (2, 6, 700), (3, 3, 2050)])
+@pytest.mark.parametrize("Bt,Dn,L", [(3, 9, 7), (3, 5, 40), (4, 3, 128), (2, 6, 700), (3, 3, 2050)])
 def test_packed_and_padded(Bt, Dn, L, dtype):
     t = inputs(Bt, Dn, L, dtype, seed=3)
-    t["reset"][0, : min(L, 30)] = True  # sequences of one token
+    t["reset"][0, : min(L // 2, 30)] = True  # sequences of one token
     t["reset"][-1, 0] = True             # h0 is cut off
     t["lengths"][0] = 0                  # a row without live steps
     t["lengths"][-1] = L
@@ -108,7 +108,7 @@ def test_packed_and_padded(Bt, Dn, L, dtype):
 
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("L,cut", [(64, 21), (900, 300), (4096, 1500)])
+@pytest.mark.parametrize("L,cut", [(13, 6), (64, 21), (127, 90), (900, 300), (4096, 1500)])
 def test_nothing_crosses_a_reset(L, cut, bad, dtype):
     """NaN or infinity in one of two packed sequences leaves the other's results as they are, both ways."""
     t = inputs(1, 3, L, dtype, seed=11)

@@ -79,6 +79,16 @@ def test_forward_and_backward(time, case, interleaved, dtype):
     run_and_check(t, freq(rot) if rot else None, True, interleaved, time, rot_scale=1.1)
 
 
+@pytest.mark.parametrize("time,case", [
+    (False, (2, 20000, 6, 2, 32, 32)), (False, (1, 30011, 5, 0, 40, 24)), (False, (3, 9001, 4, 1, 33, 18)),
+    (True, (4, 40000, 1, 1, 16, 16)), (True, (2, 24008, 2, 1, 48, 32)), (True, (1, 30001, 2, 1, 20, 20))])
+def test_long_walks(time, case):
+    """Many rows, or steps, per warp: the staging rings go round, tokens and batch elements are passed."""
+    Bt, L, Hq, Hk, D, rot = case
+    t = inputs(Bt, L, Hq, Hk, D, BF, time, seed=D, dout=F32)
+    run_and_check(t, freq(rot), True, D == 40, time, grads=(BF,))
+
+
 @pytest.mark.parametrize("time", [False, True])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_rotation_alone(dtype, time):
