@@ -1,5 +1,7 @@
 /*
- * ssm_scan.h -- C ABI of the B200 (sm_100a) selective-scan library (Mamba-1 S6).
+ * ssm_scan.h -- C ABI of the B200 (sm_100a) selective-scan library (Mamba-1 S6), of the state-space dual, and of what recurrent
+ * layers need beside them: the gated linear recurrence (ssm_lru_*), normalised and rotated queries and keys
+ * (ssm_qk_norm_rope_*).
  *
  * The operation (per batch element b, channel d, state n, time t):
  *
@@ -471,7 +473,7 @@ ssm_status ssm_lru_step(const ssm_lru_step_args *args, void *stream);
  *   (2 j, 2 j + 1) with interleaved = 1:
  *     (n_p, n_q) -> rot_scale (n_p cos - n_q sin, n_q cos + n_p sin),  angle = position * inv_freq[j]
  *   the elements from rot on pass as they are.
- * The angle and its reduction are computed in 64 bits, so positions up to 2^53 keep theirs.
+ * The angle and its reduction are computed in 64 bits: an angle of x radians is off by about x 2^-53.
  *
  * Element (b, t, h, e) of a tensor lies at b sb + h sh + t sr + e (layout SSM_QK_STATE_LAST), or
  * b sb + h sh + e sr + t (SSM_QK_TIME_LAST); strides count elements. Inputs may have any strides
