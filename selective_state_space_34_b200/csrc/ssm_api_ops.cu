@@ -197,17 +197,23 @@ ssm::QkParams qk_params(const ssm_qk_args *a) {
   return p;
 }
 
-// Time innermost: every tensor of a side with heads starts on a 16-byte boundary and steps by multiples of 8 elements.
-bool qk_vec_ok(const ssm::QkParams &p) {
-  for (int s = 0; s < 2; s++) {
-    if (p.H[s] == 0) continue;
-    for (const ssm::QkTensor *t : {&p.in[s], &p.out[s], &p.dout[s]}) {
-      if (!t->p) continue;
-      if (!aligned(t->p, 16) || (p.Bt > 1 && t->sb % 8 != 0) || (p.H[s] > 1 && t->sh % 8 != 0) || (p.D > 1 && t->sr % 8 != 0))
-        return false;
+// Time innermost: the most elements (8, 4, 2 or 1) that the strides and the addresses of both sides are multiples of, and L of 4 at
+// least with 8, of as many otherwise: a row's last run is then whole pieces of 4, 2 or 1.
+int qk_time_run(const ssm::QkParams &p) {
+  for (int V = 8; V > 1; V /= 2) {
+    bool fits = p.L % (V < 4 ? V : 4) == 0;
+    for (int s = 0; s < 2 && fits; s++) {
+      if (p.H[s] == 0) continue;
+      for (const ssm::QkTensor *t : {&p.in[s], &p.out[s], &p.dout[s]}) {
+        const size_t bytes = (size_t)V * (t->bf16 ? 2 : 4);
+        if (t->p && (!aligned(t->p, bytes < 16 ? bytes : 16) || (p.Bt > 1 && t->sb % V) || (p.H[s] > 1 && t->sh % V) ||
+                     (p.D > 1 && t->sr % V)))
+          fits = false;
+      }
     }
+    if (fits) return V;
   }
-  return true;
+  return 1;
 }
 
 ssm_status check_qk_bwd(const ssm_qk_bwd_args *a, bool *empty) {
@@ -243,7 +249,7 @@ ssm::QkParams qk_bwd_params(const ssm_qk_bwd_args *a) {
   p.out[1] = tensor(a->dk, a->dk_sb, a->dk_sh, a->dk_sr, a->grad_dtype);
   p.dw[0] = f->Hq > 0 ? a->dq_weight : nullptr;
   p.dw[1] = f->Hk > 0 ? a->dk_weight : nullptr;
-  p.vec = p.time_last && qk_vec_ok(p);
+  p.vec = p.time_last ? qk_time_run(p) : 0;
   return p;
 }
 
@@ -385,7 +391,7 @@ ssm_status ssm_qk_norm_rope_fwd(const ssm_qk_args *args, void *stream) {
   ssm::QkParams p = qk_params(args);
   p.out[0] = tensor(args->q_out, args->q_out_sb, args->q_out_sh, args->q_out_sr, args->out_dtype);
   p.out[1] = tensor(args->k_out, args->k_out_sb, args->k_out_sh, args->k_out_sr, args->out_dtype);
-  p.vec = p.time_last && qk_vec_ok(p);
+  p.vec = p.time_last ? qk_time_run(p) : 0;
   return cuda_status(ssm::launch_qk_fwd(p, args->in_dtype == SSM_BF16, static_cast<cudaStream_t>(stream)));
 }
 

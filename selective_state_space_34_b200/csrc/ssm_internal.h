@@ -187,7 +187,7 @@ struct QkParams {
   int64_t Bt, L;
   int H[2], D, rot;
   int freq_f64, pos_i64, interleaved, norm, time_last;
-  int vec;                   // time_last: 16-byte accesses
+  int vec;                   // time_last: elements that runs start at multiples of (8, 4, 2, 1)
   float eps, rot_scale, inv_D;  // inv_D = 1 / D
 };
 cudaError_t launch_qk_fwd(const QkParams &p, int in_bf16, cudaStream_t stream);

@@ -49,11 +49,6 @@ __device__ __forceinline__ void st1(void *p, int bf16, int64_t i, float v) {
   if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<float *>(p)[i] = v;
 }
-__device__ __forceinline__ void st8any(void *p, int bf16, int64_t i, const float *v) {
-  if (bf16) st8(static_cast<__nv_bfloat16 *>(p) + i, v);
-  else st8(static_cast<float *>(p) + i, v);
-}
-
 // Rows in use and asked for ahead, per group of lanes (2 to 4 measured within 3% of each other).
 template <typename T, typename Td, bool BWD> constexpr int kRowStages = BWD ? (sizeof(T) + sizeof(Td) <= 4 ? 4 : 3) : (sizeof(T) == 2 ? 4 : 3);
 
@@ -632,7 +627,7 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
 
 // m of 8 consecutive elements at i, 0 behind them; 16-byte accesses where the rows allow them and all 8 live.
 __device__ __forceinline__ void get_run(const void *p, int bf16, int64_t i, int m, int vec, float *v) {
-  if (vec && m == 8) {
+  if (vec == 8 && m == 8) {
     if (bf16) {  // cached: read again for the second pass
       Raw8<__nv_bfloat16> r;
       r.a = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
@@ -647,14 +642,17 @@ __device__ __forceinline__ void get_run(const void *p, int bf16, int64_t i, int 
 #pragma unroll
   for (int e = 0; e < 8; e++) v[e] = e < m ? ld1(p, bf16, i + e) : 0.f;
 }
-__device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, int vec, const float *v) {
-  if (vec && m == 8) {
-    st8any(p, bf16, i, v);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; e++)
-    if (e < m) st1(p, bf16, i + e, v[e]);
+// The first m of 8 elements at i (m a multiple of V), in pieces of V elements.
+__device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, int V, const float *v) {
+  auto put = [&](auto *q) {
+    using E = std::remove_reference_t<decltype(*q)>;
+    if (V == 8 && m == 8) st8(q, v);
+    else if (V >= 4) store_pieces<E, 4>(q, v, m);
+    else if (V == 2) store_pieces<E, 2>(q, v, m);
+    else store_pieces<E, 1>(q, v, m);
+  };
+  if (bf16) put(static_cast<__nv_bfloat16 *>(p) + i);
+  else put(static_cast<float *>(p) + i);
 }
 // Sums of 8 values over the 8 lanes of a warp that share bits 0 and 1 of their number, every lane ending with the sum of one
 // value (7 exchanges in place of 24).
@@ -670,9 +668,8 @@ __device__ __forceinline__ float scatter_sum(int lane, const float *v) {
 // A warp takes 32 steps of one batch element for a chunk of its heads (queries, then keys), two heads at a time: 4 lanes
 // of 8 consecutive steps, 8 lanes over the pairs, every eighth pair a lane. No barrier: a step's squares meet by shuffles.
 // Two passes over the pairs, the second from L1: the sums, then the results, with one set of cosines and sines for both
-// heads (kept over both passes and all heads where a lane has one pair, ONE). A pair unit is elements o1 and o2 (or o1
-// alone at an odd end). The backward keeps dw per warp in shared memory, each lane its own pairs'.
-template <typename T, bool BWD, bool ONE>
+// heads. A pair unit is elements o1 and o2 (or o1 alone at an odd end). The backward keeps dw per warp in shared memory, each lane its own pairs'.
+template <typename T, bool BWD>
 __global__ void __launch_bounds__(kThr, BWD ? 2 : 3)
 qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, int64_t items) {
   constexpr bool PRECISE = sizeof(T) == 4;
@@ -717,7 +714,6 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
         if (rot) turn<PRECISE>(pos[8 * tl + e], f, p.rot_scale, cs[e], sn[e]);
       }
     };
-    if (ONE && pl < n_units) angles(pl, unit_of(p, pl).rot);
     const int h_end = min(all, (int)(chunk + 1) * heads);
     for (int h0 = (int)chunk * heads; h0 < h_end; h0 += 2) {
       const int nh = min(2, h_end - h0);
@@ -742,7 +738,7 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
 #pragma unroll
             for (int e = 0; e < 8; e++) sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
             if (BWD) {
-              if (!ONE) angles(unit, u.rot);
+              angles(unit, u.rot);
               const float wa = w ? w[u.o1] : 1.f, wc = w && m2 ? w[u.o2] : 1.f;
               float ga[8], gc[8];
               get_run(dout.p, dout.bf16, dat + u.o1 * dout.sr, m, vec, ga);
@@ -766,7 +762,7 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
         const int unit = pl + 8 * n;
         const Unit u = unit_of(p, unit);
         const int m1 = u.on ? m : 0, m2 = u.on && u.o2 < p.D ? m : 0;
-        if (!ONE && u.on) angles(unit, u.rot);
+        if (u.on) angles(unit, u.rot);
 #pragma unroll 1
         for (int k = 0; k < nh; k++) {
           const int sd = h0 + k >= p.H[0], h = h0 + k - (sd ? p.H[0] : 0);
@@ -842,8 +838,8 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
   }
 }
 
-// The same for heads of up to 64 elements in 16-byte runs: the runs of the heads ahead travel in a ring of cp.async slots that
-// every lane fills and reads alone, both passes read them there, and with up to 16 elements (NP = 1) or 32 (NP = 2) a lane keeps
+// The same for heads of up to 64 elements: the runs of the heads ahead travel in a ring of cp.async slots that
+// every lane fills (in pieces of as many elements as the rows' starts are multiples of) and reads alone, both passes read them there, and with up to 16 elements (NP = 1) or 32 (NP = 2) a lane keeps
 // its NP pairs' cosines and sines for all heads of its steps.
 template <typename T, typename Td, bool BWD, int NP> struct TimeRing {
   static constexpr int kV = sizeof(T) / 2, kG = BWD ? sizeof(Td) / 2 : 0;  // 16-byte slots of a run of 8
@@ -905,20 +901,41 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
   ahead.item = (int64_t)blockIdx.x * (kThr / 32) + warp;
   open(ahead);
   Job now = ahead;
-  // 8 steps of one row into the slots from k on, element by element where not all of them live
+  // the m live ones (a multiple of V) of 8 steps of one row into the slots from k on, in pieces of V elements, 0 behind them
+  const int V = p.vec;
   auto copy = [&](int stage, int k, const auto *src, int m) {
     using E = std::remove_cv_t<std::remove_reference_t<decltype(*src)>>;
-    if (m == 8) {
+    constexpr int es = sizeof(E);
+    const char *from = reinterpret_cast<const char *>(src);
+    auto piece = [&](auto n, int at) {  // n bytes at byte `at` of the run
+      cp_async_piece<decltype(n)::value>(slot(stage, k + at / 16) + at % 16, from + at);
+    };
+    if (V == 8 && m == 8) {
 #pragma unroll
-      for (int j = 0; j < (int)sizeof(E) / 2; j++) cp_async16(slot(stage, k + j), reinterpret_cast<const char *>(src) + 16 * j);
-    } else {
-      Raw8<E> r;
-      zero8(r);
+      for (int j = 0; j < 8 * es; j += 16) piece(std::integral_constant<int, 16>(), j);
+      return;
+    }
+    if (m < 8) {  // the pieces behind the live ones; a piece is written here or by a copy, not by both
 #pragma unroll
-      for (int e = 0; e < 8; e++)
-        if (e < m) put8(r, e, src[e]);
+      for (int j = 0; j < 8; j++)
+        if (j >= m) *reinterpret_cast<E *>(slot(stage, k + j * es / 16) + j * es % 16) = from_f32<E>(0.f);
+    }
+    if (V >= 4) {
 #pragma unroll
-      for (int j = 0; j < (int)sizeof(E) / 2; j++) *reinterpret_cast<uint4 *>(slot(stage, k + j)) = reinterpret_cast<const uint4 *>(&r)[j];
+      for (int j = 0; j < 8; j += 4)
+        if (j < m) piece(std::integral_constant<int, 4 * es>(), j * es);
+    } else if (V == 2) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        if (j < m) piece(std::integral_constant<int, 2 * es>(), j * es);
+    } else if (es == 4) {
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (j < m) piece(std::integral_constant<int, 4>(), j * es);
+    } else {  // single bf16 elements have no copy of their own
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (j < m) *reinterpret_cast<E *>(slot(stage, k + j * es / 16) + j * es % 16) = src[j];
     }
   };
   auto live = [&](const Job &j) {
@@ -1067,8 +1084,8 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
           }
         }
         if (out.p) {
-          if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, 1, ga);
-          if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, 1, gc);
+          if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, V, ga);
+          if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, V, gc);
         }
       } else {
 #pragma unroll
@@ -1077,8 +1094,8 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
           a[e] = x * cs[at][e] - y * sn[at][e];
           c[e] = y * cs[at][e] + x * sn[at][e];
         }
-        if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, 1, a);
-        if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, 1, c);
+        if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, V, a);
+        if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, V, c);
       }
     }
     stage = stage == S - 1 ? 0 : stage + 1;
@@ -1252,13 +1269,13 @@ template <typename T, typename Td, bool BWD> cudaError_t time_run(const QkParams
   const int64_t most = BWD ? kBwdCtas : 3 * 148;
   *nb = (int)(ctas < most ? ctas : most);
   const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * kThr / 32 * 2 * p.D : 0;
-  if (p.vec && pairs <= 8) return time_ring<T, Td, BWD, 1>(p, *nb, heads, chunks, items, sums, s);
-  if (p.vec && pairs <= 16) return time_ring<T, Td, BWD, 2>(p, *nb, heads, chunks, items, sums, s);
-  // four pairs a lane: where the ring leaves room for two CTAs per SM
-  if constexpr (TimeRing<T, Td, BWD, 4>::kBytes <= 100 * 1024)
-    if (p.vec && pairs <= 32) return time_ring<T, Td, BWD, 4>(p, *nb, heads, chunks, items, sums, s);
-  const auto kernel = pairs <= 8 ? qk_time_kernel<T, BWD, true> : qk_time_kernel<T, BWD, false>;
-  kernel<<<*nb, kThr, sums, s>>>(p, heads, chunks, items);
+  if (pairs <= 8) return time_ring<T, Td, BWD, 1>(p, *nb, heads, chunks, items, sums, s);
+  if (pairs <= 16) return time_ring<T, Td, BWD, 2>(p, *nb, heads, chunks, items, sums, s);
+  // four pairs a lane, where the ring fits one CTA per SM at least and bf16 runs are copied, not loaded element by element
+  // (16 x 8191 steps x 64: 350 us so, 276 us from L1)
+  if constexpr (TimeRing<T, Td, BWD, 4>::kBytes <= 200 * 1024)
+    if (pairs <= 32 && (p.vec > 1 || sizeof(T) == 4)) return time_ring<T, Td, BWD, 4>(p, *nb, heads, chunks, items, sums, s);
+  qk_time_kernel<T, BWD><<<*nb, kThr, sums, s>>>(p, heads, chunks, items);
   return cudaGetLastError();
 }
 

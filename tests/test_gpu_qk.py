@@ -67,7 +67,7 @@ STATE_LAST = [(1, 1, 1, 1, 16, 16), (2, 3, 4, 1, 64, 64), (1, 5, 3, 2, 80, 48), 
               (1, 4, 8, 2, 256, 256), (2, 3, 1, 1, 1, 0), (1, 3, 2, 1, 2, 2), (2, 5, 3, 1, 33, 32), (1, 6, 2, 1, 96, 18),
               (1, 2, 1, 2, 511, 510), (3, 11, 5, 3, 24, 8), (1, 700, 8, 2, 128, 128), (2, 2500, 2, 2, 64, 32)]
 TIME_LAST = [(1, 1, 1, 1, 16, 16), (2, 8, 1, 1, 16, 16), (1, 13, 2, 1, 4, 4), (2, 264, 1, 1, 64, 64), (1, 40, 2, 2, 128, 64),
-             (2, 77, 1, 0, 33, 18), (1, 515, 1, 1, 16, 8), (1, 16, 1, 1, 512, 512), (1, 24, 1, 2, 1, 0), (2, 2304, 1, 1, 16, 16)]
+             (2, 77, 1, 0, 33, 18), (2, 36, 1, 1, 16, 16), (1, 50, 2, 1, 24, 24), (3, 18, 3, 0, 64, 64), (2, 20, 1, 1, 40, 20), (1, 515, 1, 1, 16, 8), (1, 16, 1, 1, 512, 512), (1, 24, 1, 2, 1, 0), (2, 2304, 1, 1, 16, 16)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
