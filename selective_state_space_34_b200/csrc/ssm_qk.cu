@@ -20,9 +20,9 @@
 // and sines; a step's squares meet by shuffles.
 //
 // Angles. In 32 bits position * inv_freq loses the angle of a far position (at 10^6 the spacing is 1/16 of
-// a radian), so the product and its reduction to a fraction of a turn are in 64 bits; what is left
-// goes through the hardware sine (absolute error 2^-21) for bf16, sincospif for fp32 inputs. An angle of x radians
-// is off by about x 2^-53 and those.
+// a radian). A frequency is kept as turns per position in units of 2^-64, so that the product with the position modulo 2^64 is
+// the reduced angle, exact but for the frequency's rounding in 64 bits (an angle of x radians is off by about x 2^-53);
+// what is left goes through the hardware sine (absolute error 2^-21) for bf16, sincospif for fp32 inputs.
 //
 // What bounds it. HBM by its bytes; issue in fact (66% and 59% of the slots: 17 a element forwards, 25 backwards, of which the
 // angles are 1 to 6 by the number of heads that share them). 2 x 4096 tokens x 40 heads x 128, bf16: forward 36 us (4.7 TB/s), backward
@@ -53,25 +53,25 @@ __device__ __forceinline__ void st1(void *p, int bf16, int64_t i, float v) {
 template <typename T, typename Td, bool BWD> constexpr int kRowStages = BWD ? (sizeof(T) + sizeof(Td) <= 4 ? 4 : 3) : (sizeof(T) == 2 ? 4 : 3);
 
 // Of token b L + t.
-__device__ __forceinline__ double position(const QkParams &p, int64_t token, int64_t t) {
-  if (!p.pos) return (double)(p.pos0 + t);
-  return p.pos_i64 ? (double)static_cast<const int64_t *>(p.pos)[token]
-                   : (double)static_cast<const int32_t *>(p.pos)[token];
+__device__ __forceinline__ int64_t position(const QkParams &p, int64_t token, int64_t t) {
+  if (!p.pos) return p.pos0 + t;
+  return p.pos_i64 ? static_cast<const int64_t *>(p.pos)[token] : (int64_t)static_cast<const int32_t *>(p.pos)[token];
 }
-// Turns per position of pair j.
-__device__ __forceinline__ double frequency(const QkParams &p, int j) {
-  return kInvTwoPi *
-         (p.freq_f64 ? static_cast<const double *>(p.inv_freq)[j] : (double)static_cast<const float *>(p.inv_freq)[j]);
+// Turns per position of pair j, in units of 2^-64 turns modulo 1.
+__device__ __forceinline__ uint64_t frequency(const QkParams &p, int j) {
+  const double f = kInvTwoPi *
+                   (p.freq_f64 ? static_cast<const double *>(p.inv_freq)[j] : (double)static_cast<const float *>(p.inv_freq)[j]);
+  return (uint64_t)((f - floor(f)) * 18446744073709551616.0);
 }
-// Cosine and sine of pos * f turns, times the scale.
+// Cosine and sine of pos * f turns, times the scale. The product modulo 2^64 is the angle's fraction of a turn, whatever the
+// position and its sign.
 template <bool PRECISE>
-__device__ __forceinline__ void turn(double pos, double f, float scale, float &c, float &s) {
-  const double t = pos * f;
-  const float frac = (float)(t - rint(t));  // a fraction of a turn in [-1/2, 1/2]
+__device__ __forceinline__ void turn(int64_t pos, uint64_t f, float scale, float &c, float &s) {
+  const float frac = (float)(int32_t)(((uint64_t)pos * f) >> 32);  // in 2^-32 turns, from -1/2 to 1/2
   if (PRECISE) {
-    sincospif(2.f * frac, &s, &c);
+    sincospif(frac * 0x1p-31f, &s, &c);
   } else {
-    const float x = frac * 6.283185307179586f;
+    const float x = frac * (6.283185307179586f * 0x1p-32f);
     c = __cosf(x);
     s = __sinf(x);
   }
@@ -204,11 +204,12 @@ struct Place {
 template <typename... P>
 __device__ __forceinline__ bool advance(Walk &w, int dt, int dh, int H, int L, P &...places) {
   w.h += dh;
+  ((places.at += places.step), ...);
+  if (dt == 0 && w.h < H) return false;  // the common step: another head of the token
   const bool more = w.h >= H;
   const int moved = dt + (more ? 1 : 0);
   w.t += moved;
   w.token += moved;
-  ((places.at += places.step), ...);
   if (more) {
     w.h -= H;
     ((places.at += places.wrap), ...);
@@ -217,7 +218,7 @@ __device__ __forceinline__ bool advance(Walk &w, int dt, int dh, int H, int L, P
     w.t -= L;
     ((places.at += places.turn), ...);
   }
-  return moved != 0;
+  return true;
 }
 // Sums over the G lanes of a row.
 template <typename... F> __device__ __forceinline__ void sum_lanes(int G, F &...v) {
@@ -274,7 +275,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   constexpr bool kAll = !INTER && V == 8;  // all 8 of a rotated unit (the half layout's run starts are then multiples of 8)
   // in shared memory, by unit: the weights of its pairs' members, and its pairs' turns per position
   __shared__ float4 sw[4][32];
-  __shared__ double sf[8][32];
+  __shared__ uint64_t sf[8][32];
   for (int j = threadIdx.x; j < 16 * G; j += kThr) {  // lanes without a unit read weights too: 1, which their zeros stay 0 with
     const int u = j >> 4, e = j & 15;
     int a1, a2, m1, m2;
@@ -368,6 +369,9 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
       store_pieces<float, V>(q + gap, v + 8, n2);
     }
   };
+  // given positions: the next token's is loaded when a token begins, where the walk says which it is
+  const bool known = p.pos && rot && (dt == 0 || dh == 0);
+  int64_t coming = known && grp < n_rows ? position(p, now.token, now.t) : 0;
   __syncthreads();
   int stage = 0;
   bool fresh = true;
@@ -375,7 +379,11 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
     const bool live = i + grp < n_rows;
     fetch(stage == 0 ? S - 1 : stage - 1);
     if (fresh && rot && live) {
-      const double pos = position(p, now.token, now.t);
+      const int64_t pos = known ? coming : position(p, now.token, now.t);
+      if (known) {
+        const int64_t token = min(now.token + (dt ? dt : 1), p.Bt * p.L - 1);
+        coming = position(p, token, 0);
+      }
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         if (kAll || 2 * j < turned) turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
@@ -560,7 +568,7 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
       }
     fetch();
     if (fresh && live && p.rot) {
-      const double pos = position(p, now.token, now.t);
+      const int64_t pos = position(p, now.token, now.t);
 #pragma unroll
       for (int n = 0; n < NU; n++)
         if (rot[n]) turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c[n], s[n]);
@@ -683,9 +691,9 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
   }
   float *const mine = sdw + warp * 2 * p.D;
   // per warp: the positions of its 32 steps, and for each of two heads their 1 / rms and factors of the input's part of a gradient
-  __shared__ double positions[kThr / 32][32];
+  __shared__ int64_t positions[kThr / 32][32];
   __shared__ __align__(16) float factors[kThr / 32][BWD ? 4 : 2][32];
-  double *const pos = positions[warp];
+  int64_t *const pos = positions[warp];
   const int own = 8 * tl + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);  // the step whose sum this lane ends with
   auto factor = [&](int k, float *v) {
     const float4 *f = reinterpret_cast<const float4 *>(&factors[warp][k][8 * tl]);
@@ -702,11 +710,11 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
     const int m = (int)(p.L - t0 < 0 ? 0 : p.L - t0 < 8 ? p.L - t0 : 8);  // live steps of this lane
     const int64_t t_own = tt * 32 + lane;
     __syncwarp();  // the item before is done with them
-    pos[lane] = p.rot && t_own < p.L ? position(p, b * p.L + t_own, t_own) : 0.0;
+    pos[lane] = p.rot && t_own < p.L ? position(p, b * p.L + t_own, t_own) : 0;
     __syncwarp();
     float cs[8], sn[8];
     auto angles = [&](int unit, bool rot) {
-      const double f = rot ? frequency(p, unit) : 0.0;
+      const uint64_t f = rot ? frequency(p, unit) : 0;
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         cs[e] = 1.f;
@@ -844,7 +852,7 @@ qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, in
 template <typename T, typename Td, bool BWD, int NP> struct TimeRing {
   static constexpr int kV = sizeof(T) / 2, kG = BWD ? sizeof(Td) / 2 : 0;  // 16-byte slots of a run of 8
   static constexpr int kSlots = 2 * NP * (kV + kG), kStageBytes = kSlots * 512;  // of a lane; of a warp
-  static constexpr int S = kStageBytes <= 3072 ? 4 : kStageBytes <= 4096 ? 3 : 2;
+  static constexpr int S = kStageBytes <= 3 << 10 ? 4 : kStageBytes <= 4 << 10 ? 3 : 2;
   static constexpr int kBytes = kThr / 32 * S * kStageBytes;
 };
 template <typename T, typename Td, bool BWD, int NP>
@@ -862,7 +870,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
     for (int j = threadIdx.x; j < kThr / 32 * 2 * p.D; j += kThr) sdw[j] = 0.f;
     __syncthreads();
   }
-  __shared__ double positions[kThr / 32][32];
+  __shared__ int64_t positions[kThr / 32][32];
   __shared__ __align__(16) float factors[kThr / 32][BWD ? 2 : 1][32];
   char *const base = smem + warp * S * Ring::kStageBytes + lane * 16;
   auto slot = [&](int stage, int k) { return base + (stage * Ring::kSlots + k) * 512; };
@@ -978,7 +986,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
   constexpr int kKeep = NP <= 2 ? NP : 1;  // pairs whose angles are kept
   float cs[kKeep][8], sn[kKeep][8];
   auto angles = [&](int n, int at) {
-    const double f = u[n].on && u[n].rot ? frequency(p, pl + 8 * n) : 0.0;
+    const uint64_t f = u[n].on && u[n].rot ? frequency(p, pl + 8 * n) : 0;
 #pragma unroll
     for (int e = 0; e < 8; e++) {
       cs[at][e] = 1.f;
@@ -994,7 +1002,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
     if (fresh) {
       __syncwarp();  // the item before is done with the positions
       const int64_t t = now.t0 + lane;
-      positions[warp][lane] = p.rot && t < p.L ? position(p, now.b * p.L + t, t) : 0.0;
+      positions[warp][lane] = p.rot && t < p.L ? position(p, now.b * p.L + t, t) : 0;
       __syncwarp();
       if (NP <= 2) {
 #pragma unroll
