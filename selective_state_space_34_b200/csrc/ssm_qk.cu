@@ -16,8 +16,8 @@
 // its squares by shuffles. Where runs start at multiples of 4 or 2 elements only, they travel in 8- or 4-byte pieces of the same
 // units; odd head sizes take units of one pair.
 //
-// Time innermost (time_last): a warp owns 32 consecutive steps and walks the pairs and heads, two heads on one set of cosines
-// and sines; a step's squares meet by shuffles.
+// Time innermost (time_last): a warp owns 32 consecutive steps of 8 or 16 pairs and walks the heads on one set of cosines and
+// sines; a step's squares meet by shuffles, and across the warps of a larger head through shared memory.
 //
 // Angles. In 32 bits position * inv_freq loses the angle of a far position (at 10^6 the spacing is 1/16 of
 // a radian). A frequency is kept as turns per position in units of 2^-64, so that the product with the position modulo 2^64 is
@@ -39,12 +39,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThr = 256;                 // threads per CTA
-constexpr int kBwdCtas = 148 * 2;         // most CTAs of a backward (each keeps a share of dw)
+constexpr int kCtas = 148 * 2;            // most CTAs of a backward (each keeps a share of dw) and of a rows forward
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-__device__ __forceinline__ float ld1(const void *p, int bf16, int64_t i) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
-}
 __device__ __forceinline__ void st1(void *p, int bf16, int64_t i, float v) {
   if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<float *>(p)[i] = v;
@@ -153,6 +150,11 @@ template <typename T, int V> __device__ __forceinline__ void store_pieces(T *p, 
   }
 }
 // N bytes on their way to shared memory.
+// The first n (2 or 4) bytes of a 4-byte word, 0 in the others.
+__device__ __forceinline__ void cp_async_part(void *dst, const void *src, int n) {
+  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(src), "r"(n));
+}
 template <int N> __device__ __forceinline__ void cp_async_piece(void *dst, const void *src) {
   if constexpr (N == 16) {
     cp_async16(dst, src);
@@ -236,7 +238,7 @@ template <typename... F> __device__ __forceinline__ void sum_lanes(int G, F &...
 // recomputed where the token changes; pairs that are not rotated keep 1 and 0. The backward adds its share of dw over all its
 // rows.
 template <typename T, typename Td, bool BWD, bool INTER, int V>
-__global__ void __launch_bounds__(kThr, BWD ? 2 : 3)
+__global__ void __launch_bounds__(kThr, 2)
 qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0, int64_t per1) {
   constexpr bool PRECISE = sizeof(T) == 4;
   constexpr int kSlotsV = sizeof(T), kSlotsG = BWD ? sizeof(Td) : 0;  // 16-byte slots of 16 elements
@@ -633,23 +635,6 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
 
 // ---- time innermost ----------------------------------------------------------------------------
 
-// m of 8 consecutive elements at i, 0 behind them; 16-byte accesses where the rows allow them and all 8 live.
-__device__ __forceinline__ void get_run(const void *p, int bf16, int64_t i, int m, int vec, float *v) {
-  if (vec == 8 && m == 8) {
-    if (bf16) {  // cached: read again for the second pass
-      Raw8<__nv_bfloat16> r;
-      r.a = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-      unpack8(r, v);
-    } else {
-      Raw8<float> r;
-      ld8(static_cast<const float *>(p) + i, r);
-      unpack8(r, v);
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; e++) v[e] = e < m ? ld1(p, bf16, i + e) : 0.f;
-}
 // The first m of 8 elements at i (m a multiple of V), in pieces of V elements.
 __device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, int V, const float *v) {
   auto put = [&](auto *q) {
@@ -664,7 +649,8 @@ __device__ __forceinline__ void put_run(void *p, int bf16, int64_t i, int m, int
 }
 // Sums of 8 values over the 8 lanes of a warp that share bits 0 and 1 of their number, every lane ending with the sum of one
 // value (7 exchanges in place of 24).
-__device__ __forceinline__ float scatter_sum(int lane, const float *v) {
+__device__ __forceinline__ float scatter_sum(int lane, const float2 *f) {
+  const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
   float a[4], b[2];
   const bool h4 = lane & 16, h2 = lane & 8, h1 = lane & 4;
 #pragma unroll
@@ -673,251 +659,122 @@ __device__ __forceinline__ float scatter_sum(int lane, const float *v) {
   for (int e = 0; e < 2; e++) b[e] = (h2 ? a[e + 2] : a[e]) + __shfl_xor_sync(kFull, h2 ? a[e] : a[e + 2], 8);
   return (h1 ? b[1] : b[0]) + __shfl_xor_sync(kFull, h1 ? b[0] : b[1], 4);
 }
-// A warp takes 32 steps of one batch element for a chunk of its heads (queries, then keys), two heads at a time: 4 lanes
-// of 8 consecutive steps, 8 lanes over the pairs, every eighth pair a lane. No barrier: a step's squares meet by shuffles.
-// Two passes over the pairs, the second from L1: the sums, then the results, with one set of cosines and sines for both
-// heads. A pair unit is elements o1 and o2 (or o1 alone at an odd end). The backward keeps dw per warp in shared memory, each lane its own pairs'.
-template <typename T, bool BWD>
-__global__ void __launch_bounds__(kThr, BWD ? 2 : 3)
-qk_time_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, int64_t items) {
-  constexpr bool PRECISE = sizeof(T) == 4;
-  extern __shared__ float sdw[];  // (warps, 2, D) with dw
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane & 3, pl = lane >> 2;
-  const int n_units = p.rot / 2 + (p.D - p.rot + 1) / 2, all = p.H[0] + p.H[1], vec = p.vec;
-  const bool sums = BWD && p.norm && (p.dw[0] || p.dw[1]);
-  if (sums) {
-    for (int j = threadIdx.x; j < kThr / 32 * 2 * p.D; j += kThr) sdw[j] = 0.f;
-    __syncthreads();
-  }
-  float *const mine = sdw + warp * 2 * p.D;
-  // per warp: the positions of its 32 steps, and for each of two heads their 1 / rms and factors of the input's part of a gradient
-  __shared__ int64_t positions[kThr / 32][32];
-  __shared__ __align__(16) float factors[kThr / 32][BWD ? 4 : 2][32];
-  int64_t *const pos = positions[warp];
-  const int own = 8 * tl + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);  // the step whose sum this lane ends with
-  auto factor = [&](int k, float *v) {
-    const float4 *f = reinterpret_cast<const float4 *>(&factors[warp][k][8 * tl]);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  };
-  const int64_t per_row = (p.L + 31) / 32;
-  for (int64_t item = (int64_t)blockIdx.x * (kThr / 32) + warp; item < items; item += (int64_t)gridDim.x * (kThr / 32)) {
-    int64_t bc, tt, b, chunk;
-    divide(item, per_row, bc, tt);
-    divide(bc, chunks, b, chunk);
-    const int64_t t0 = tt * 32 + 8 * tl;
-    const int m = (int)(p.L - t0 < 0 ? 0 : p.L - t0 < 8 ? p.L - t0 : 8);  // live steps of this lane
-    const int64_t t_own = tt * 32 + lane;
-    __syncwarp();  // the item before is done with them
-    pos[lane] = p.rot && t_own < p.L ? position(p, b * p.L + t_own, t_own) : 0;
-    __syncwarp();
-    float cs[8], sn[8];
-    auto angles = [&](int unit, bool rot) {
-      const uint64_t f = rot ? frequency(p, unit) : 0;
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        cs[e] = 1.f;
-        sn[e] = 0.f;
-        if (rot) turn<PRECISE>(pos[8 * tl + e], f, p.rot_scale, cs[e], sn[e]);
-      }
-    };
-    const int h_end = min(all, (int)(chunk + 1) * heads);
-    for (int h0 = (int)chunk * heads; h0 < h_end; h0 += 2) {
-      const int nh = min(2, h_end - h0);
-      // pass 1: the squares, and backwards the products with the gradients turned back
-      if (p.norm) {
-        __syncwarp();  // the heads before are done with the factors
-#pragma unroll 1
-        for (int k = 0; k < nh; k++) {
-          const int sd = h0 + k >= p.H[0], h = h0 + k - (sd ? p.H[0] : 0);
-          const QkTensor &in = p.in[sd], &dout = p.dout[sd];
-          const int64_t at = b * in.sb + h * in.sh + t0, dat = BWD ? b * dout.sb + h * dout.sh + t0 : 0;
-          const float *w = p.w[sd];
-          float sc[8], back[8];
-#pragma unroll
-          for (int e = 0; e < 8; e++) sc[e] = back[e] = 0.f;
-          for (int unit = pl; unit < n_units; unit += 8) {
-            const Unit u = unit_of(p, unit);
-            const int m2 = u.o2 < p.D ? m : 0;
-            float a[8], c[8];
-            get_run(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m, vec, a);
-            get_run(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, m2, vec, c);
-#pragma unroll
-            for (int e = 0; e < 8; e++) sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
-            if (BWD) {
-              angles(unit, u.rot);
-              const float wa = w ? w[u.o1] : 1.f, wc = w && m2 ? w[u.o2] : 1.f;
-              float ga[8], gc[8];
-              get_run(dout.p, dout.bf16, dat + u.o1 * dout.sr, m, vec, ga);
-              get_run(dout.p, dout.bf16, dat + u.o2 * dout.sr, m2, vec, gc);
-#pragma unroll
-              for (int e = 0; e < 8; e++) {
-                const float x = ga[e] * cs[e] + gc[e] * sn[e], y = gc[e] * cs[e] - ga[e] * sn[e];
-                back[e] = fmaf(x * wa, a[e], fmaf(y * wc, c[e], back[e]));
-              }
-            }
-          }
-          const float r = inv_rms(p, scatter_sum(lane, sc));
-          factors[warp][k][own] = r;
-          if (BWD) factors[warp][2 + k][own] = r * r * scatter_sum(lane, back) * p.inv_D;
-        }
-        __syncwarp();
-      }
-      // pass 2
-      const int rounds = (n_units + 7) / 8;
-      for (int n = 0; n < rounds; n++) {
-        const int unit = pl + 8 * n;
-        const Unit u = unit_of(p, unit);
-        const int m1 = u.on ? m : 0, m2 = u.on && u.o2 < p.D ? m : 0;
-        if (u.on) angles(unit, u.rot);
-#pragma unroll 1
-        for (int k = 0; k < nh; k++) {
-          const int sd = h0 + k >= p.H[0], h = h0 + k - (sd ? p.H[0] : 0);
-          const QkTensor &in = p.in[sd], &out = p.out[sd];
-          const int64_t at = b * in.sb + h * in.sh + t0, oat = b * out.sb + h * out.sh + t0;
-          const float *w = p.w[sd];
-          const float wa = w && u.on ? w[u.o1] : 1.f, wc = w && m2 ? w[u.o2] : 1.f;
-          float sc[8], back[8];
-          if (p.norm) {
-            factor(k, sc);
-            if (BWD) factor(2 + k, back);
-          }
-          float a[8], c[8];
-          if (!BWD || p.norm) {
-            get_run(in.p, PRECISE ? 0 : 1, at + u.o1 * in.sr, m1, vec, a);
-            get_run(in.p, PRECISE ? 0 : 1, at + u.o2 * in.sr, m2, vec, c);
-          }
-          if (BWD) {
-            const QkTensor &dout = p.dout[sd];
-            const int64_t dat = b * dout.sb + h * dout.sh + t0;
-            float ga[8], gc[8];
-            get_run(dout.p, dout.bf16, dat + u.o1 * dout.sr, m1, vec, ga);
-            get_run(dout.p, dout.bf16, dat + u.o2 * dout.sr, m2, vec, gc);
-            float dx = 0.f, dy = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-              const float x = ga[e] * cs[e] + gc[e] * sn[e], y = gc[e] * cs[e] - ga[e] * sn[e];
-              ga[e] = x;
-              gc[e] = y;
-              if (p.norm) {
-                if (e < m1) {  // a step that is none has no 1 / sqrt(0) either
-                  dx = fmaf(x * sc[e], a[e], dx);
-                  dy = fmaf(y * sc[e], c[e], dy);
-                }
-                ga[e] = sc[e] * (x * wa - a[e] * back[e]);
-                gc[e] = sc[e] * (y * wc - c[e] * back[e]);
-              }
-            }
-            if (sums) {  // over the 4 lanes of a pair; the first of them owns its place
-              dx += __shfl_xor_sync(kFull, dx, 1);
-              dy += __shfl_xor_sync(kFull, dy, 1);
-              dx += __shfl_xor_sync(kFull, dx, 2);
-              dy += __shfl_xor_sync(kFull, dy, 2);
-              if (tl == 0 && u.on) {
-                mine[sd * p.D + u.o1] += dx;
-                if (u.o2 < p.D) mine[sd * p.D + u.o2] += dy;
-              }
-            }
-            if (out.p) {
-              put_run(out.p, out.bf16, oat + u.o1 * out.sr, m1, vec, ga);
-              put_run(out.p, out.bf16, oat + u.o2 * out.sr, m2, vec, gc);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-              const float x = p.norm ? a[e] * (sc[e] * wa) : a[e], y = p.norm ? c[e] * (sc[e] * wc) : c[e];
-              a[e] = x * cs[e] - y * sn[e];
-              c[e] = y * cs[e] + x * sn[e];
-            }
-            put_run(out.p, out.bf16, oat + u.o1 * out.sr, m1, vec, a);
-            put_run(out.p, out.bf16, oat + u.o2 * out.sr, m2, vec, c);
-          }
-        }
-      }
-    }
-  }
-  if (!sums) return;
-  __syncthreads();  // the block's shares, rows 2 block + side: the warps' in their order
-  for (int j = threadIdx.x; j < 2 * p.D; j += kThr) {
-    float t = 0.f;
-    for (int w = 0; w < kThr / 32; w++) t += sdw[w * 2 * p.D + j];
-    p.part[2 * (int64_t)blockIdx.x * p.D + j] = t;
-  }
-}
-
-// The same for heads of up to 64 elements: the runs of the heads ahead travel in a ring of cp.async slots that
-// every lane fills (in pieces of as many elements as the rows' starts are multiples of) and reads alone, both passes read them there, and with up to 16 elements (NP = 1) or 32 (NP = 2) a lane keeps
-// its NP pairs' cosines and sines for all heads of its steps.
-template <typename T, typename Td, bool BWD, int NP> struct TimeRing {
+// W warps take 32 steps of one batch element for a chunk of its heads (queries, then keys), each warp 8 NP of the pairs, 4 lanes
+// of 8 consecutive steps by 8 lanes of NP pairs. A pair unit is elements o1 and o2 (or o1 alone at an odd end). The
+// runs of the heads ahead travel in a ring of cp.async slots that every lane fills (in pieces of as many elements as the rows'
+// starts are multiples of) and reads alone. A lane keeps its pairs' cosines and sines for all heads of its steps; a step's squares
+// meet by shuffles, and those of W > 1 warps through shared memory, with one barrier of theirs a head.
+// Single bf16 elements have no copy of their own: a run off the 4-byte boundary travels as the five words around it, of which the
+// first and last are copied only as far as the row goes; the fifth words have slots of their own.
+template <typename T, typename Td, bool BWD, int NP, bool FULL> struct TimeRing {
   static constexpr int kV = sizeof(T) / 2, kG = BWD ? sizeof(Td) / 2 : 0;  // 16-byte slots of a run of 8
-  static constexpr int kSlots = 2 * NP * (kV + kG), kStageBytes = kSlots * 512;  // of a lane; of a warp
-  static constexpr int S = kStageBytes <= 3 << 10 ? 4 : kStageBytes <= 4 << 10 ? 3 : 2;
-  static constexpr int kBytes = kThr / 32 * S * kStageBytes;
+  static constexpr int kRuns = 2 * NP * (kV + kG), kFifth = FULL ? 0 : 2 * NP * ((kV == 1) + (kG == 1));
+  static constexpr int kSlots = kRuns + (kFifth + 3) / 4, kStageBytes = kSlots * 512;  // of a lane; of a warp
+  static constexpr int S = kStageBytes <= 3 << 10 ? 4 : kStageBytes <= 4 << 10 ? 3 : kStageBytes <= 6 << 10 ? 2 : 1;  // 128 KB
+  static constexpr int kWarpBytes = S * kStageBytes;
 };
-template <typename T, typename Td, bool BWD, int NP>
-__global__ void __launch_bounds__(kThr, BWD || NP == 2 ? 2 : 3)
-qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunks, int64_t items) {
+// How the steps are cut: warps a slice of 32, its heads at a time, their chunks, slices of a batch element; and the batch
+// elements, chunks and slices from one item of a group of warps to its next.
+struct TimePlan {
+  int W, heads, chunks, per_row, dchunk, dtt;
+  int64_t db;
+};
+template <typename T, typename Td, bool BWD, int NP, bool FULL>
+__global__ void __launch_bounds__(NP == 2 ? 2 * kThr : kThr, NP == 2 ? 1 : BWD || !FULL ? 2 : 3)
+qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ TimePlan plan) {
+  const int W = plan.W;
   constexpr bool PRECISE = sizeof(T) == 4;
-  using Ring = TimeRing<T, Td, BWD, NP>;
-  constexpr int S = Ring::S, kV = Ring::kV, kG = Ring::kG;
+  using Ring = TimeRing<T, Td, BWD, NP, FULL>;
+  constexpr int S = Ring::S, kV = Ring::kV, kG = Ring::kG, kMost = NP == 2 ? kThr / 16 : kThr / 32;  // most warps
   extern __shared__ __align__(16) char smem[];  // the ring, then (warps, 2, D) sums of dw
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane & 3, pl = lane >> 2;
   const int all = p.H[0] + p.H[1];
   const bool sums = BWD && p.norm && (p.dw[0] || p.dw[1]), reads_v = !BWD || p.norm;
-  float *const sdw = reinterpret_cast<float *>(smem + Ring::kBytes), *const mine = sdw + warp * 2 * p.D;
-  if (sums) {
-    for (int j = threadIdx.x; j < kThr / 32 * 2 * p.D; j += kThr) sdw[j] = 0.f;
-    __syncthreads();
-  }
-  __shared__ int64_t positions[kThr / 32][32];
-  __shared__ __align__(16) float factors[kThr / 32][BWD ? 2 : 1][32];
-  char *const base = smem + warp * S * Ring::kStageBytes + lane * 16;
+  const int groups = blockDim.x / 32 / W, group = warp / W, first = group * W;  // warps left over have no group
+  float *const sdw = reinterpret_cast<float *>(smem + blockDim.x / 32 * Ring::kWarpBytes);
+  float acc[2][NP][2];  // this lane's share of dw, by side
+#pragma unroll
+  for (int n = 0; n < NP; n++) acc[0][n][0] = acc[0][n][1] = acc[1][n][0] = acc[1][n][1] = 0.f;
+  __shared__ float shares[2][kMost][BWD ? 2 : 1][32];  // the warps' sums of each step, for this head and the one before
+  __shared__ int64_t positions[kMost][32];
+  __shared__ __align__(16) float factors[kMost][BWD ? 2 : 1][32];
+  char *const base = smem + warp * Ring::kWarpBytes + lane * 16;
   auto slot = [&](int stage, int k) { return base + (stage * Ring::kSlots + k) * 512; };
   Unit u[NP];
 #pragma unroll
-  for (int n = 0; n < NP; n++) u[n] = unit_of(p, pl + 8 * n);
+  for (int n = 0; n < NP; n++) u[n] = unit_of(p, pl + 8 * (warp - first + n * W));
 #pragma unroll
   for (int k = 0; k < S * Ring::kSlots; k++) *reinterpret_cast<uint4 *>(slot(0, k)) = make_uint4(0, 0, 0, 0);
   const int own = 8 * tl + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);  // the step whose sum this lane ends with
-  // one head of one item at a time
+  // one head of one item at a time; items are numbered batch element, chunk of heads, slice of 32 steps, the last fastest
   struct Job {
-    int64_t item, b, t0;  // t0: of the warp
-    int h, h_end;
+    int64_t b, t0;  // t0: of the warps
+    int tt, chunk, h, h_end;
     bool on;
   };
-  const int64_t per_row = (p.L + 31) / 32, stride = (int64_t)gridDim.x * (kThr / 32);
   auto open = [&](Job &j) {
-    j.on = j.item < items;
-    if (!j.on) return;
-    int64_t bc, tt, chunk;
-    divide(j.item, per_row, bc, tt);
-    divide(bc, chunks, j.b, chunk);
-    j.t0 = tt * 32;
-    j.h = (int)chunk * heads;
-    j.h_end = min(all, j.h + heads);
+    j.on = j.b < p.Bt;
+    j.t0 = (int64_t)j.tt * 32;
+    j.h = j.chunk * plan.heads;
+    j.h_end = min(all, j.h + plan.heads);
   };
   auto next = [&](Job &j) {
-    if (++j.h == j.h_end) {
-      j.item += stride;
-      open(j);
-      return true;
+    if (++j.h < j.h_end) return false;
+    j.tt += plan.dtt;
+    j.chunk += plan.dchunk;
+    j.b += plan.db;
+    if (j.tt >= plan.per_row) {
+      j.tt -= plan.per_row;
+      j.chunk++;
     }
-    return false;
+    if (j.chunk >= plan.chunks) {
+      j.chunk -= plan.chunks;
+      j.b++;
+    }
+    open(j);
+    return true;
   };
   Job ahead;
-  ahead.item = (int64_t)blockIdx.x * (kThr / 32) + warp;
+  int64_t bc, left;
+  divide((int64_t)blockIdx.x * groups + group, plan.per_row, bc, left);
+  ahead.tt = (int)left;
+  divide(bc, plan.chunks, ahead.b, left);
+  ahead.chunk = (int)left;
+  if (group >= groups) ahead.b = p.Bt;
   open(ahead);
   Job now = ahead;
-  // the m live ones (a multiple of V) of 8 steps of one row into the slots from k on, in pieces of V elements, 0 behind them
   const int V = p.vec;
-  auto copy = [&](int stage, int k, const auto *src, int m) {
+  constexpr int kFifthG = kV == 1 ? 2 * NP : 0;  // the gradients' first
+  auto fifth = [&](int stage, int run) { return reinterpret_cast<uint32_t *>(slot(stage, Ring::kRuns + run / 4) + run % 4 * 4); };
+  // the m live ones (a multiple of V) of 8 steps of one row into the slots from k on, in pieces of V elements, 0 behind them;
+  // run: its fifth word; begin: of the row
+  auto copy = [&](int stage, int k, int run, const auto *src, int m, bool begin) {
     using E = std::remove_cv_t<std::remove_reference_t<decltype(*src)>>;
     constexpr int es = sizeof(E);
     const char *from = reinterpret_cast<const char *>(src);
     auto piece = [&](auto n, int at) {  // n bytes at byte `at` of the run
       cp_async_piece<decltype(n)::value>(slot(stage, k + at / 16) + at % 16, from + at);
     };
+    if constexpr (FULL) {
+#pragma unroll
+      for (int j = 0; j < 8 * es; j += 16) {
+        if (m) cp_async_piece<16>(slot(stage, k + j / 16), from + j);
+        else *reinterpret_cast<uint4 *>(slot(stage, k + j / 16)) = make_uint4(0, 0, 0, 0);
+      }
+      return;
+    }
+    if (es == 2 && V == 1) {
+      const int odd = (int)(reinterpret_cast<uintptr_t>(src) >> 1 & 1);
+#pragma unroll
+      for (int j = 0; j < 5; j++) {  // elements 2 j - odd and the one behind it
+        uint32_t *const to = j < 4 ? reinterpret_cast<uint32_t *>(slot(stage, k)) + j : fifth(stage, run);
+        const int n = m ? min(2, m - 2 * j + odd) : 0;
+        if (j == 0 && odd && begin) *to = m ? (uint32_t)*reinterpret_cast<const uint16_t *>(src) << 16 : 0;
+        else if (n > 0) cp_async_part(to, from + 4 * j - 2 * odd, 2 * n);
+        else *to = 0;
+      }
+      return;
+    }
     if (V == 8 && m == 8) {
 #pragma unroll
       for (int j = 0; j < 8 * es; j += 16) piece(std::integral_constant<int, 16>(), j);
@@ -940,10 +797,6 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
 #pragma unroll
       for (int j = 0; j < 8; j++)
         if (j < m) piece(std::integral_constant<int, 4>(), j * es);
-    } else {  // single bf16 elements have no copy of their own
-#pragma unroll
-      for (int j = 0; j < 8; j++)
-        if (j < m) *reinterpret_cast<E *>(slot(stage, k + j * es / 16) + j * es % 16) = src[j];
     }
   };
   auto live = [&](const Job &j) {
@@ -961,40 +814,79 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
         if (reads_v) {
           const QkTensor &x = p.in[sd];
           const T *a = static_cast<const T *>(x.p) + ahead.b * x.sb + h * x.sh + t;
-          copy(stage, 2 * n * kV, a + u[n].o1 * x.sr, m);
-          if (two) copy(stage, (2 * n + 1) * kV, a + u[n].o2 * x.sr, m);
+          copy(stage, 2 * n * kV, 2 * n, a + u[n].o1 * x.sr, m, t == 0);
+          if (two) copy(stage, (2 * n + 1) * kV, 2 * n + 1, a + u[n].o2 * x.sr, m, t == 0);
         }
         if (BWD) {
           const QkTensor &x = p.dout[sd];
           const Td *a = static_cast<const Td *>(x.p) + ahead.b * x.sb + h * x.sh + t;
-          copy(stage, 2 * NP * kV + 2 * n * kG, a + u[n].o1 * x.sr, m);
-          if (two) copy(stage, 2 * NP * kV + (2 * n + 1) * kG, a + u[n].o2 * x.sr, m);
+          copy(stage, 2 * NP * kV + 2 * n * kG, kFifthG + 2 * n, a + u[n].o1 * x.sr, m, t == 0);
+          if (two) copy(stage, 2 * NP * kV + (2 * n + 1) * kG, kFifthG + 2 * n + 1, a + u[n].o2 * x.sr, m, t == 0);
         }
       }
       next(ahead);
     }
     cp_async_commit();
   };
-  auto take = [&](int stage, int k, auto tag, float *v) {
+  // a run of row o of x
+  auto take = [&](int stage, int k, int run, auto tag, const QkTensor &x, int64_t head, int o, float2 *f) {
     Raw8<decltype(tag)> r;
+    float v[8];
 #pragma unroll
     for (int j = 0; j < (int)sizeof(tag) / 2; j++) reinterpret_cast<uint4 *>(&r)[j] = *reinterpret_cast<const uint4 *>(slot(stage, k + j));
+    if constexpr (!FULL && sizeof(tag) == 2) {
+      const uint32_t at = (uint32_t)(reinterpret_cast<uintptr_t>(x.p) >> 1) + (uint32_t)head + (uint32_t)o * (uint32_t)x.sr;
+      if (V == 1) {
+        const uint32_t by = at & 1 ? 0x5432 : 0x3210, w[5] = {r.a.x, r.a.y, r.a.z, r.a.w, *fifth(stage, run)};
+        r.a = make_uint4(__byte_perm(w[0], w[1], by), __byte_perm(w[1], w[2], by), __byte_perm(w[2], w[3], by), __byte_perm(w[3], w[4], by));
+      }
+    }
     unpack8(r, v);
+#pragma unroll
+    for (int e = 0; e < 4; e++) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
   };
 #pragma unroll
   for (int j = 0; j < S - 1; j++) fetch(j);
-  constexpr int kKeep = NP <= 2 ? NP : 1;  // pairs whose angles are kept
-  float cs[kKeep][8], sn[kKeep][8];
-  auto angles = [&](int n, int at) {
-    const uint64_t f = u[n].on && u[n].rot ? frequency(p, pl + 8 * n) : 0;
+  __shared__ uint64_t freq[kMost][NP][8];  // by pair
+  float2 cs[NP][4], sn[NP][4];
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      cs[at][e] = 1.f;
-      sn[at][e] = 0.f;
-      if (u[n].on && u[n].rot) turn<PRECISE>(positions[warp][8 * tl + e], f, p.rot_scale, cs[at][e], sn[at][e]);
+  for (int n = 0; n < NP; n++) {
+    if (tl == 0 && u[n].on && u[n].rot) freq[warp][n][pl] = frequency(p, pl + 8 * (warp - first + n * W));
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      cs[n][e] = splat(1.f);
+      sn[n][e] = splat(0.f);
+    }
+  }
+  // the m live ones of 8 results of one row at i
+  auto put = [&](const QkTensor &x, int64_t i, int m, const float2 *f) {
+    const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+    if constexpr (FULL) {
+      if (!m) return;
+      if (x.bf16) st8(static_cast<__nv_bfloat16 *>(x.p) + i, v);
+      else st8(static_cast<float *>(x.p) + i, v);
+    } else if (V == 1 && m == 8 && x.bf16) {  // three whole words, then another or the elements at both ends
+      char *const to = static_cast<char *>(x.p) + 2 * i;
+      const int odd = (int)(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t *>(&b);
+      }
+#pragma unroll
+      for (int e = 0; e < 3; e++) *reinterpret_cast<uint32_t *>(to + 4 * e + 2 * odd) = odd ? __byte_perm(w[e], w[e + 1], 0x5432) : w[e];
+      if (odd) {
+        *reinterpret_cast<uint16_t *>(to) = (uint16_t)w[0];
+        *reinterpret_cast<uint16_t *>(to + 14) = (uint16_t)(w[3] >> 16);
+      } else {
+        *reinterpret_cast<uint32_t *>(to + 12) = w[3];
+      }
+    } else {
+      put_run(x.p, x.bf16, i, m, V, v);
     }
   };
-  int stage = 0;
+  int stage = 0, half = 0;
   bool fresh = true;
   while (now.on) {
     fetch(stage == 0 ? S - 1 : stage - 1);
@@ -1004,117 +896,142 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, int heads, int64_t chunk
       const int64_t t = now.t0 + lane;
       positions[warp][lane] = p.rot && t < p.L ? position(p, now.b * p.L + t, t) : 0;
       __syncwarp();
-      if (NP <= 2) {
 #pragma unroll
-        for (int n = 0; n < kKeep; n++) angles(n, n);
-      }
+      for (int n = 0; n < NP; n++)
+        if (u[n].on && u[n].rot) {
+          const uint64_t f = freq[warp][n][pl];
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            turn<PRECISE>(positions[warp][8 * tl + 2 * e], f, p.rot_scale, cs[n][e].x, sn[n][e].x);
+            turn<PRECISE>(positions[warp][8 * tl + 2 * e + 1], f, p.rot_scale, cs[n][e].y, sn[n][e].y);
+          }
+        }
     }
     cp_async_wait<S - 1>();
     const float *w = p.w[sd];
-    float sc[8], back[8];
+    const QkTensor &in = p.in[sd], &dout = p.dout[sd];
+    const int64_t at = now.b * in.sb + h * in.sh, dat = now.b * dout.sb + h * dout.sh;
+    // one pair's elements, and backwards its gradients turned back
+    float2 a[4], c[4], ga[4], gc[4];
+    float wa, wc;
+    auto pair = [&](int n) {
+      wa = w && u[n].on ? w[u[n].o1] : 1.f;
+      wc = w && u[n].on && u[n].o2 < p.D ? w[u[n].o2] : 1.f;
+      if (reads_v) {
+        take(stage, 2 * n * kV, 2 * n, T(), in, at, u[n].o1, a);
+        take(stage, (2 * n + 1) * kV, 2 * n + 1, T(), in, at, u[n].o2, c);
+      }
+      if constexpr (BWD) {
+        take(stage, 2 * NP * kV + 2 * n * kG, kFifthG + 2 * n, Td(), dout, dat, u[n].o1, ga);
+        take(stage, 2 * NP * kV + (2 * n + 1) * kG, kFifthG + 2 * n + 1, Td(), dout, dat, u[n].o2, gc);
 #pragma unroll
-    for (int e = 0; e < 8; e++) sc[e] = back[e] = 0.f;
+        for (int e = 0; e < 4; e++) {
+          const float2 x = ga[e], y = gc[e];
+          ga[e] = fma2(y, sn[n][e], mul2(x, cs[n][e]));
+          gc[e] = fma2(x, neg2(sn[n][e]), mul2(y, cs[n][e]));
+        }
+      }
+    };
+    float2 sc[4], back[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) sc[e] = back[e] = splat(0.f);
     if (p.norm) {
 #pragma unroll
       for (int n = 0; n < NP; n++) {
-        float a[8], c[8];
-        take(stage, 2 * n * kV, T(), a);
-        take(stage, (2 * n + 1) * kV, T(), c);
+        pair(n);
 #pragma unroll
-        for (int e = 0; e < 8; e++) sc[e] = fmaf(a[e], a[e], fmaf(c[e], c[e], sc[e]));
-        if constexpr (BWD) {
-          constexpr bool keep = NP <= 2;
-          if (!keep) angles(n, 0);
-          const int at = keep ? n : 0;
-          const float wa = w && u[n].on ? w[u[n].o1] : 1.f, wc = w && u[n].on && u[n].o2 < p.D ? w[u[n].o2] : 1.f;
-          float ga[8], gc[8];
-          take(stage, 2 * NP * kV + 2 * n * kG, Td(), ga);
-          take(stage, 2 * NP * kV + (2 * n + 1) * kG, Td(), gc);
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const float x = ga[e] * cs[at][e] + gc[e] * sn[at][e], y = gc[e] * cs[at][e] - ga[e] * sn[at][e];
-            back[e] = fmaf(x * wa, a[e], fmaf(y * wc, c[e], back[e]));
-          }
+        for (int e = 0; e < 4; e++) {
+          sc[e] = fma2(a[e], a[e], fma2(c[e], c[e], sc[e]));
+          if (BWD) back[e] = fma2(mul2(ga[e], splat(wa)), a[e], fma2(mul2(gc[e], splat(wc)), c[e], back[e]));
         }
       }
-      const float r = inv_rms(p, scatter_sum(lane, sc));
-      const float q = BWD ? r * r * scatter_sum(lane, back) * p.inv_D : 0.f;
+      float sum = scatter_sum(lane, sc), dot = BWD ? scatter_sum(lane, back) : 0.f;
+      int step = own;  // of the 32, whose sums these are
+      if (W > 1) {
+        shares[half][warp][0][own] = sum;
+        if (BWD) shares[half][warp][BWD ? 1 : 0][own] = dot;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * W) : "memory");
+        step = lane;
+        sum = dot = 0.f;
+        for (int j = first; j < first + W; j++) {
+          sum += shares[half][j][0][lane];
+          if (BWD) dot += shares[half][j][BWD ? 1 : 0][lane];
+        }
+        half ^= 1;  // written again two heads on: everyone has passed the barrier between
+      }
+      const float r = now.t0 + step < p.L ? inv_rms(p, sum) : 0.f;  // with an eps of 0, 1 / sqrt(0) of a step that is none
       __syncwarp();  // the head before is done with the factors
-      factors[warp][0][own] = r;
-      if (BWD) factors[warp][BWD ? 1 : 0][own] = q;
+      factors[warp][0][step] = r;
+      if (BWD) factors[warp][BWD ? 1 : 0][step] = -r * r * r * dot * p.inv_D;
       __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; e++) {
-        sc[e] = factors[warp][0][8 * tl + e];
-        if (BWD) back[e] = factors[warp][BWD ? 1 : 0][8 * tl + e];
+      for (int e = 0; e < 4; e++) {
+        sc[e] = *reinterpret_cast<const float2 *>(&factors[warp][0][8 * tl + 2 * e]);
+        if (BWD) back[e] = *reinterpret_cast<const float2 *>(&factors[warp][BWD ? 1 : 0][8 * tl + 2 * e]);
       }
     }
     const QkTensor &out = p.out[sd];
     const int64_t to = now.b * out.sb + h * out.sh + now.t0 + 8 * tl;
 #pragma unroll
     for (int n = 0; n < NP; n++) {
-      const bool two = u[n].on && u[n].o2 < p.D;
-      constexpr bool keep = NP <= 2;
-      if (!keep) angles(n, 0);
-      const int at = keep ? n : 0;
-      const float wa = w && u[n].on ? w[u[n].o1] : 1.f, wc = w && two ? w[u[n].o2] : 1.f;
-      float a[8], c[8];
-      if (reads_v) {
-        take(stage, 2 * n * kV, T(), a);
-        take(stage, (2 * n + 1) * kV, T(), c);
-      }
+      if (NP > 1 || !p.norm) pair(n);  // one pair is still here
       if constexpr (BWD) {
-        float ga[8], gc[8], dx = 0.f, dy = 0.f;
-        take(stage, 2 * NP * kV + 2 * n * kG, Td(), ga);
-        take(stage, 2 * NP * kV + (2 * n + 1) * kG, Td(), gc);
+        if (p.norm) {
+          float2 dx = splat(0.f), dy = splat(0.f);
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const float x = ga[e] * cs[at][e] + gc[e] * sn[at][e], y = gc[e] * cs[at][e] - ga[e] * sn[at][e];
-          ga[e] = x;
-          gc[e] = y;
-          if (p.norm) {
-            if (e < m) {  // a step that is none has no 1 / sqrt(0) either
-              dx = fmaf(x * sc[e], a[e], dx);
-              dy = fmaf(y * sc[e], c[e], dy);
-            }
-            ga[e] = sc[e] * (x * wa - a[e] * back[e]);
-            gc[e] = sc[e] * (y * wc - c[e] * back[e]);
+          for (int e = 0; e < 4; e++) {
+            const float2 x = mul2(ga[e], sc[e]), y = mul2(gc[e], sc[e]);
+            dx = fma2(x, a[e], dx);
+            dy = fma2(y, c[e], dy);
+            a[e] = fma2(a[e], back[e], mul2(x, splat(wa)));
+            c[e] = fma2(c[e], back[e], mul2(y, splat(wc)));
           }
-        }
-        if (sums) {  // over the 4 lanes of a pair; the first of them owns its place
-          dx += __shfl_xor_sync(kFull, dx, 1);
-          dy += __shfl_xor_sync(kFull, dy, 1);
-          dx += __shfl_xor_sync(kFull, dx, 2);
-          dy += __shfl_xor_sync(kFull, dy, 2);
-          if (tl == 0 && u[n].on) {
-            mine[sd * p.D + u[n].o1] += dx;
-            if (two) mine[sd * p.D + u[n].o2] += dy;
+          acc[0][n][0] += sd ? 0.f : dx.x + dx.y;
+          acc[0][n][1] += sd ? 0.f : dy.x + dy.y;
+          acc[1][n][0] += sd ? dx.x + dx.y : 0.f;
+          acc[1][n][1] += sd ? dy.x + dy.y : 0.f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            a[e] = ga[e];
+            c[e] = gc[e];
           }
-        }
-        if (out.p) {
-          if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, V, ga);
-          if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, V, gc);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const float x = p.norm ? a[e] * (sc[e] * wa) : a[e], y = p.norm ? c[e] * (sc[e] * wc) : c[e];
-          a[e] = x * cs[at][e] - y * sn[at][e];
-          c[e] = y * cs[at][e] + x * sn[at][e];
+        for (int e = 0; e < 4; e++) {
+          const float2 x = p.norm ? mul2(a[e], mul2(sc[e], splat(wa))) : a[e], y = p.norm ? mul2(c[e], mul2(sc[e], splat(wc))) : c[e];
+          a[e] = fma2(y, neg2(sn[n][e]), mul2(x, cs[n][e]));
+          c[e] = fma2(x, sn[n][e], mul2(y, cs[n][e]));
         }
-        if (u[n].on) put_run(out.p, out.bf16, to + u[n].o1 * out.sr, m, V, a);
-        if (two) put_run(out.p, out.bf16, to + u[n].o2 * out.sr, m, V, c);
+      }
+      if (out.p && u[n].on) {
+        put(out, to + u[n].o1 * out.sr, m, a);
+        if (u[n].o2 < p.D) put(out, to + u[n].o2 * out.sr, m, c);
       }
     }
     stage = stage == S - 1 ? 0 : stage + 1;
     fresh = next(now);
   }
-  if (!sums) return;
-  __syncthreads();  // the block's shares, rows 2 block + side: the warps' in their order
-  for (int j = threadIdx.x; j < 2 * p.D; j += kThr) {
-    float t = 0.f;
-    for (int w = 0; w < kThr / 32; w++) t += sdw[w * 2 * p.D + j];
-    p.part[2 * (int64_t)blockIdx.x * p.D + j] = t;
+  if constexpr (BWD) {
+    if (!sums) return;
+    // the block's shares, rows 2 block + side: a pair's over its 4 lanes, then the groups' in their order
+#pragma unroll
+    for (int n = 0; n < NP; n++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int sd = j >> 1, at = sd * p.D + (j & 1 ? u[n].o2 : u[n].o1);
+        float v = acc[sd][n][j & 1];
+        v += __shfl_xor_sync(kFull, v, 1);
+        v += __shfl_xor_sync(kFull, v, 2);
+        if (tl == 0 && group < groups && u[n].on && (!(j & 1) || u[n].o2 < p.D)) sdw[group * 2 * p.D + at] = v;
+      }
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * p.D; j += blockDim.x) {
+      float t = 0.f;
+      for (int g = 0; g < groups; g++) t += sdw[g * 2 * p.D + j];
+      p.part[2 * (int64_t)blockIdx.x * p.D + j] = t;
+    }
   }
 }
 
@@ -1127,14 +1044,14 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const __grid_constant__ QkP
   if (!p.dw[side]) return;
   const int j = blockIdx.x * 32 + x, n = side ? n1 : n0;
   const float *part = p.part + (side ? (int64_t)lo1 * p.D : 0);
-  float v[kBwdCtas / 32 + 1], s = 0.f;
+  float v[kCtas / 32 + 1], s = 0.f;
 #pragma unroll
-  for (int k = 0; k < kBwdCtas / 32 + 1; k++) {
+  for (int k = 0; k < kCtas / 32 + 1; k++) {
     const int at = y + 32 * k;
     v[k] = j < p.D && at < n ? part[(int64_t)at * stride * p.D + j] : 0.f;
   }
 #pragma unroll
-  for (int k = 0; k < kBwdCtas / 32 + 1; k++) s += v[k];
+  for (int k = 0; k < kCtas / 32 + 1; k++) s += v[k];
   red[y][x] = s;
   __syncthreads();
   s = red[x][y];  // element y's shares
@@ -1205,10 +1122,11 @@ struct RowPlan {
   int V, G, nb0, nb;
   int64_t per[2];
 };
-bool plan_rows(const QkParams &p, int64_t most, RowPlan *r) {
+bool plan_rows(const QkParams &p, bool bwd, RowPlan *r) {
   constexpr int kWarps = kThr / 32;
   r->V = run_of(p);
   r->G = lanes_per_row(p, r->V);
+  const int64_t most = bwd || r->V ? kCtas : 3 * 148;
   const int step = 32 / r->G;
   int64_t rows[2], work[2];
   int n[2];
@@ -1238,9 +1156,11 @@ template <typename K> cudaError_t launch_rows(K kernel, const QkParams &p, const
   return cudaGetLastError();
 }
 
-// Head elements innermost, forward (Td = T) or backward. CTAs: what fits the SMs at once.
+// Head elements innermost, forward (Td = T) or backward. CTAs: what fits the SMs at once, two each, three where a
+// forward goes by pairs. (Three forward CTAs of runs an SM, which leaves 80 registers and a few spills: 4 x 4096 tokens x 4
+// heads of 64, 8.5 us against 7.7; 2 x 4096 x 40 of 128 alike.)
 template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams &p, RowPlan *r, cudaStream_t s) {
-  if (!plan_rows(p, BWD ? kBwdCtas : 3 * 148, r)) return cudaErrorInvalidConfiguration;
+  if (!plan_rows(p, BWD, r)) return cudaErrorInvalidConfiguration;
   const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * (kThr / r->G) * p.D : 0;
   constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
   constexpr int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>;
@@ -1257,34 +1177,38 @@ template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams
   return launch_rows(pairs_of(p) <= 128 ? qk_pairs_kernel<T, Td, BWD, 4> : qk_pairs_kernel<T, Td, BWD, 8>, p, *r, sums, s);
 }
 
-// Time innermost. All heads of a batch element go to one warp, for their common angles, where that leaves 16 warps per SM. CTAs:
-// what fits the SMs at once (the backward's each keep a share of dw of both sides).
+// Time innermost. All heads of a batch element go to one group of warps, for their common angles, where that leaves 16 warps
+// per SM. CTAs: what fits the SMs at once (the backward's each keep a share of dw of both sides).
 template <typename T, typename Td, bool BWD, int NP>
-cudaError_t time_ring(const QkParams &p, int nb, int heads, int64_t chunks, int64_t items, int sums, cudaStream_t s) {
-  const auto kernel = qk_time_ring_kernel<T, Td, BWD, NP>;
-  const int smem = TimeRing<T, Td, BWD, NP>::kBytes + sums;
+cudaError_t time_ring(const QkParams &p, const TimePlan &plan, int nb, int warps, int sums, cudaStream_t s) {
+  const bool full = p.vec == 8 && p.L % 8 == 0;
+  const auto kernel = full ? qk_time_ring_kernel<T, Td, BWD, NP, true> : qk_time_ring_kernel<T, Td, BWD, NP, false>;
+  const int smem = warps * (full ? TimeRing<T, Td, BWD, NP, true>::kWarpBytes : TimeRing<T, Td, BWD, NP, false>::kWarpBytes) + sums;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<nb, kThr, smem, s>>>(p, heads, chunks, items);
+  kernel<<<nb, 32 * warps, smem, s>>>(p, plan);
   return cudaGetLastError();
 }
 
 template <typename T, typename Td, bool BWD> cudaError_t time_run(const QkParams &p, int *nb, cudaStream_t s) {
-  const int64_t slices = p.Bt * ((p.L + 31) / 32);
   const int all = p.H[0] + p.H[1], pairs = pairs_of(p);
-  const int heads = slices >= 16 * 148 ? all : slices * 2 >= 16 * 148 && all > 2 ? 2 : 1;
-  const int64_t chunks = (all + heads - 1) / heads, items = slices * chunks, ctas = (items + kThr / 32 - 1) / (kThr / 32);
-  const int64_t most = BWD ? kBwdCtas : 3 * 148;
+  // one pair a lane where eight warps hold them all, else two, of up to sixteen warps
+  const int NP = pairs <= kThr / 4 ? 1 : 2, warps = pairs <= kThr / 2 ? kThr / 32 : kThr / 16;
+  TimePlan t;
+  t.W = (pairs + 8 * NP - 1) / (8 * NP);
+  t.per_row = (int)((p.L + 31) / 32);
+  const int64_t slices = p.Bt * t.per_row;
+  t.heads = slices * t.W >= 16 * 148 ? all : slices * t.W * 2 >= 16 * 148 && all > 2 ? 2 : 1;
+  t.chunks = (all + t.heads - 1) / t.heads;
+  const int groups = warps / t.W;
+  const int64_t ctas = (slices * t.chunks + groups - 1) / groups, most = BWD ? kCtas : 3 * 148;
   *nb = (int)(ctas < most ? ctas : most);
-  const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * kThr / 32 * 2 * p.D : 0;
-  if (pairs <= 8) return time_ring<T, Td, BWD, 1>(p, *nb, heads, chunks, items, sums, s);
-  if (pairs <= 16) return time_ring<T, Td, BWD, 2>(p, *nb, heads, chunks, items, sums, s);
-  // four pairs a lane, where the ring fits one CTA per SM at least and bf16 runs are copied, not loaded element by element
-  // (16 x 8191 steps x 64: 350 us so, 276 us from L1)
-  if constexpr (TimeRing<T, Td, BWD, 4>::kBytes <= 200 * 1024)
-    if (pairs <= 32 && (p.vec > 1 || sizeof(T) == 4)) return time_ring<T, Td, BWD, 4>(p, *nb, heads, chunks, items, sums, s);
-  qk_time_kernel<T, BWD><<<*nb, kThr, sums, s>>>(p, heads, chunks, items);
-  return cudaGetLastError();
+  const int64_t stride = (int64_t)*nb * groups;
+  t.dtt = (int)(stride % t.per_row);
+  t.dchunk = (int)(stride / t.per_row % t.chunks);
+  t.db = stride / t.per_row / t.chunks;
+  const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * groups * 2 * p.D : 0;
+  return NP == 1 ? time_ring<T, Td, BWD, 1>(p, t, *nb, warps, sums, s) : time_ring<T, Td, BWD, 2>(p, t, *nb, warps, sums, s);
 }
 
 template <typename T> cudaError_t fwd_t(const QkParams &p, cudaStream_t s) {
@@ -1313,10 +1237,10 @@ template <typename T> cudaError_t bwd_t(const QkParams &p, cudaStream_t s) {
 
 }  // namespace
 
-// Whatever the plan: at most kBwdCtas shares, one more where a side rounds up from none; two from each of kBwdCtas CTAs with
-// time innermost. (qk_dw_kernel reads up to kBwdCtas + 32 - kBwdCtas % 32 of a side.)
+// Whatever the plan: at most kCtas shares, one more where a side rounds up from none; two from each of kCtas CTAs with
+// time innermost. (qk_dw_kernel reads up to kCtas + 32 - kCtas % 32 of a side.)
 size_t qk_bwd_workspace_bytes(const QkParams &p) {
-  return p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(2 * kBwdCtas + 2) * (size_t)p.D : 0;
+  return p.dw[0] || p.dw[1] ? sizeof(float) * (size_t)(2 * kCtas + 2) * (size_t)p.D : 0;
 }
 
 cudaError_t launch_qk_fwd(const QkParams &p, int in_bf16, cudaStream_t s) {

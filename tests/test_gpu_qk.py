@@ -89,6 +89,48 @@ def test_long_walks(time, case):
     run_and_check(t, freq(rot), True, D == 40, time, grads=(BF,))
 
 
+@pytest.mark.parametrize("dtype,dout", [(F32, F32), (BF, BF), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("case", [(2, 75, 1, 1, 66, 66), (1, 37, 2, 1, 200, 150), (1, 40, 2, 1, 136, 136), (1, 24, 1, 1, 300, 128),
+                                  (2, 35, 1, 2, 511, 20), (1, 64, 2, 0, 384, 384), (3, 8203, 1, 1, 40, 40),
+                                  (300, 5, 2, 1, 96, 94), (40, 64, 3, 2, 18, 18)])
+def test_warps_share_steps(case, dtype, dout):
+    """Time innermost: heads of several warps, with warps to spare, two pairs a lane, and more items than groups of warps."""
+    Bt, L, Hq, Hk, D, rot = case
+    t = inputs(Bt, L, Hq, Hk, D, dtype, True, seed=D + L, dout=dout)
+    run_and_check(t, freq(rot), True, D % 4 == 2, True, grads=(BF,) if L > 100 else (F32, BF))
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("L", [1, 7, 8, 33, 64, 71])
+@pytest.mark.parametrize("begin", [0, 1])
+def test_rows_off_their_boundaries(L, begin, out):
+    """Time innermost, bf16 rows of odd strides or starts: what lies around the rows is neither used nor written."""
+    t = inputs(2, L, 2, 1, 24, BF, True, seed=L)
+    whole = {}
+    for n in ("q", "k", "dq_out", "dk_out"):  # rows of L + 2 - begin elements, NaN around the live ones
+        v = t[n]
+        whole[n] = torch.full(v.shape[:-1] + (L + 2 - begin,), float("nan"), dtype=BF, device="cuda")
+        t[n] = whole[n][..., begin:begin + L].copy_(v)
+    kw = dict(inv_freq=freq(24), positions=t["positions"], q_weight=t["q_weight"], k_weight=t["k_weight"], layout="bhdl")
+    want = ssm.ssm_qk_norm_rope_fwd(t["q"].contiguous(), t["k"].contiguous(), out_dtype=out, **kw)
+    base = [torch.full_like(whole[n], 7.0, dtype=out) for n in ("q", "k")]
+    views = tuple(b[..., begin:begin + L] for b in base)
+    ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], out_dtype=out, out=views, **kw)
+    for b, v, w in zip(base, views, want):
+        assert torch.equal(v, w)
+        assert (b[..., :begin] == 7).all() and (b[..., begin + L:] == 7).all()
+    args = ("dq_out", "q", "dk_out", "k")
+    g = ssm.ssm_qk_norm_rope_bwd(*[t[n] for n in args], grad_dtype=out, **kw)
+    w = ssm.ssm_qk_norm_rope_bwd(*[t[n].contiguous() for n in args], grad_dtype=out, **kw)
+    for n in w:
+        assert torch.equal(g[n], w[n]), n
+    if out == BF:  # in place
+        ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], out=(t["q"], t["k"]), **kw)
+        for n, v in zip("qk", want):
+            assert torch.equal(t[n], v)
+            assert whole[n][..., :begin].isnan().all() and whole[n][..., begin + L:].isnan().all()
+
+
 @pytest.mark.parametrize("time", [False, True])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_rotation_alone(dtype, time):
