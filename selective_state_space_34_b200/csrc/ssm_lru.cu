@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(32 * W, W <= 4 ? 28 / W : 1) lru_fwd_kernel(co
 // ---- backward ----------------------------------------------------------------------------------
 
 template <typename T, typename Tg, int W, bool RESET>
-__global__ void __launch_bounds__(32 * W, W <= 4 ? 16 / W : 1) lru_bwd_kernel(const __grid_constant__ LruBwdParams q) {
+__global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(const __grid_constant__ LruBwdParams q) {
   const LruParams &p = q.f;
   extern __shared__ __align__(16) char ring_smem[];
   constexpr int S = kStages<T, W>;
@@ -691,13 +691,17 @@ template <bool CUT> __device__ __forceinline__ void scan_down_group(int gl, int 
   }
 }
 
+__device__ __forceinline__ int64_t batch_of(int64_t row, int64_t Dn) {
+  return (row | Dn) >> 32 ? row / Dn : (int64_t)((uint32_t)row / (uint32_t)Dn);
+}
+
 template <typename T, typename Tout, bool RESET>
-__global__ void __launch_bounds__(128) lru_fwd_short_kernel(const __grid_constant__ LruParams p, int G) {
-  const int64_t rows = p.Bt * p.Dn, id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / G;
-  const int gl = threadIdx.x & (G - 1);
+__global__ void __launch_bounds__(128) lru_fwd_short_kernel(const __grid_constant__ LruParams p, int lg) {
+  const int G = 1 << lg, gl = threadIdx.x & (G - 1);
+  const int64_t rows = p.Bt * p.Dn, id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> lg;
   const bool live = id < rows;
   const int64_t row = live ? id : rows - 1;  // groups behind the last row follow along on it and store nothing
-  const int64_t b = row / p.Dn, d = row - b * p.Dn;
+  const int64_t b = batch_of(row, p.Dn), d = row - b * p.Dn;
   const Row R = row_of(p, row, b);
   const int64_t total = rows * p.L;
   const int t0 = 8 * gl - R.f, L = (int)p.L;
@@ -719,10 +723,16 @@ __global__ void __launch_bounds__(128) lru_fwd_short_kernel(const __grid_constan
     decay<false>(fma2(r[j], splat(rate), splat(kTiny)), a[j], sq, is);
     bb[j] = mul2(mul2(mul2(sq, is), g[j]), bb[j]);
   }
+  const bool in = t0 >= 0 && t0 + 8 <= R.len;
+  if (!in) {
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    if (t0 + e < 0 || t0 + e >= R.len) elem(a, e) = 1.f, elem(bb, e) = 0.f;
-    if (RESET && (cut >> (8 * e) & 0xff)) elem(a, e) = 0.f;
+    for (int e = 0; e < 8; e++)
+      if (t0 + e < 0 || t0 + e >= R.len) elem(a, e) = 1.f, elem(bb, e) = 0.f;
+  }
+  if (RESET && cut) {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (cut >> (8 * e) & 0xff) elem(a, e) = 0.f;
   }
   float2 P2, H2;
   compose<RESET>(a, bb, P2, H2);
@@ -738,21 +748,23 @@ __global__ void __launch_bounds__(128) lru_fwd_short_kernel(const __grid_constan
   if (p.states && gl == 0) p.states[row * p.n_states] = h0;
   if (p.h_last && gl == G - 1) p.h_last[row] = h.y;
   if (p.out) {
+    if (!in) {
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-      if (t0 + e >= R.len) elem(bb, e) = 0.f;
-    store_group(static_cast<Tout *>(p.out), R, false, t0, L, p.vec_out, bb);
+      for (int e = 0; e < 8; e++)
+        if (t0 + e >= R.len) elem(bb, e) = 0.f;
+    }
+    store_group(static_cast<Tout *>(p.out), R, in, t0, L, p.vec_out, bb);
   }
 }
 
 template <typename T, typename Tg, bool RESET>
-__global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constant__ LruBwdParams q, int G) {
+__global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constant__ LruBwdParams q, int lg) {
   const LruParams &p = q.f;
-  const int64_t rows = p.Bt * p.Dn, id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / G;
-  const int gl = threadIdx.x & (G - 1);
+  const int G = 1 << lg, gl = threadIdx.x & (G - 1);
+  const int64_t rows = p.Bt * p.Dn, id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> lg;
   const bool live = id < rows;
   const int64_t row = live ? id : rows - 1;
-  const int64_t b = row / p.Dn, d = row - b * p.Dn;
+  const int64_t b = batch_of(row, p.Dn), d = row - b * p.Dn;
   const Row R = row_of(p, row, b);
   const int64_t total = rows * p.L;
   const int t0 = 8 * gl - R.f, L = (int)p.L;
@@ -782,13 +794,19 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
     v[j] = mul2(bb[j], mul2(ev, g));
     z[j] = mul2(mul2(mul2(y[j], is), is), bb[j]);
   }
+  const bool in = t0 >= 0 && t0 + 8 <= R.len;
+  if (!in) {
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    if (t0 + e < 0 || t0 + e >= R.len) {
-      elem(a, e) = 1.f;
-      elem(bb, e) = elem(y, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
-    }
-    if (RESET && (cut >> (8 * e) & 0xff)) elem(a, e) = 0.f;
+    for (int e = 0; e < 8; e++)
+      if (t0 + e < 0 || t0 + e >= R.len) {
+        elem(a, e) = 1.f;
+        elem(bb, e) = elem(y, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+      }
+  }
+  if (RESET && cut) {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (cut >> (8 * e) & 0xff) elem(a, e) = 0.f;
   }
   float2 P2, H2, M2 = splat(0.f);
   compose<RESET>(a, bb, P2, H2);
@@ -821,9 +839,11 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
     bb[j] = mul2(z[j], lm);
     z[j] = mul2(bb[j], fma2(y[j], splat(inv_rate), splat(-1.f)));
   }
+  if (!in) {  // steps outside the row hold 0 (0 times an infinite lambda would not be)
 #pragma unroll
-  for (int e = 0; e < 8; e++)  // steps outside the row hold 0 (0 times an infinite lambda would not be)
-    if (t0 + e < 0 || t0 + e >= R.len) elem(u, e) = elem(v, e) = elem(z, e) = elem(bb, e) = 0.f;
+    for (int e = 0; e < 8; e++)
+      if (t0 + e < 0 || t0 + e >= R.len) elem(u, e) = elem(v, e) = elem(z, e) = elem(bb, e) = 0.f;
+  }
   float2 sq2 = splat(0.f), sr2 = splat(0.f), si2 = splat(0.f);
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -838,9 +858,9 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
     si += __shfl_xor_sync(kFull, si, off);
   }
   if (!live) return;
-  if (q.dx) store_group(static_cast<Tg *>(q.dx), R, false, t0, L, q.vec_grad, u);
-  if (q.di) store_group(static_cast<Tg *>(q.di), R, false, t0, L, q.vec_grad, v);
-  if (q.dr) store_group(static_cast<Tg *>(q.dr), R, false, t0, L, q.vec_grad, z);
+  if (q.dx) store_group(static_cast<Tg *>(q.dx), R, in, t0, L, q.vec_grad, u);
+  if (q.di) store_group(static_cast<Tg *>(q.di), R, in, t0, L, q.vec_grad, v);
+  if (q.dr) store_group(static_cast<Tg *>(q.dr), R, in, t0, L, q.vec_grad, z);
   if (gl) return;
   if (q.dh0) q.dh0[row] = mu.x;
   const float sp = softplus<true>(lam);
@@ -849,19 +869,21 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
   if (q.p_di) q.p_di[row] = si;
 }
 
-// Per-row sums over the batch in a fixed order.
+// Per-row sums over the batch in a fixed order, eight loads in flight. blockIdx.y: dlam, dr_bias or di_bias.
 __global__ void __launch_bounds__(128) lru_param_sum_kernel(const __grid_constant__ LruBwdParams q) {
   const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= q.f.Dn) return;
-  const float *src[3] = {q.p_dlam, q.p_dr, q.p_di};
-  float *dst[3] = {q.dlam, q.dr_bias, q.di_bias};
+  const float *src = blockIdx.y == 0 ? q.p_dlam : blockIdx.y == 1 ? q.p_dr : q.p_di;
+  float *dst = blockIdx.y == 0 ? q.dlam : blockIdx.y == 1 ? q.dr_bias : q.di_bias;
+  if (d >= q.f.Dn || !dst) return;
+  float s = 0.f;
+  for (int64_t b0 = 0; b0 < q.f.Bt; b0 += 8) {
+    float v[8];
 #pragma unroll
-  for (int j = 0; j < 3; j++) {
-    if (!dst[j]) continue;
-    float s = 0.f;
-    for (int64_t b = 0; b < q.f.Bt; b++) s += src[j][b * q.f.Dn + d];
-    dst[j][d] = s;
+    for (int j = 0; j < 8; j++) v[j] = b0 + j < q.f.Bt ? src[(b0 + j) * q.f.Dn + d] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) s += v[j];
   }
+  dst[d] = s;
 }
 
 // ---- one-token step ----------------------------------------------------------------------------
@@ -942,13 +964,13 @@ template <typename K> cudaError_t allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Lanes per row of the short-row kernels, 0 for longer rows.
+// Lanes per row of the short-row kernels, as a power of two; -1 for longer rows.
 int short_lanes(int64_t L) {
   const int64_t groups = (L + (L % 8 ? 7 : 0) + 7) / 8;  // rows of whole groups start on one
-  if (groups > 16) return 0;
-  int g = 1;
-  while (g < groups) g *= 2;
-  return g;
+  if (groups > 16) return -1;
+  int lg = 0;
+  while (1 << lg < groups) lg++;
+  return lg;
 }
 
 template <typename T, typename Tout, int W>
@@ -963,11 +985,11 @@ cudaError_t fwd_w(const LruParams &p, cudaStream_t s) {
 }
 
 template <typename T, typename Tout> cudaError_t fwd_t(const LruParams &p, cudaStream_t s) {
-  if (const int G = short_lanes(p.L)) {
-    const int64_t blocks = (p.Bt * p.Dn * G + 127) / 128;
+  if (const int lg = short_lanes(p.L); lg >= 0) {
+    const int64_t blocks = (((p.Bt * p.Dn) << lg) + 127) / 128;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const auto kernel = p.reset ? lru_fwd_short_kernel<T, Tout, true> : lru_fwd_short_kernel<T, Tout, false>;
-    kernel<<<(unsigned)blocks, 128, 0, s>>>(p, G);
+    kernel<<<(unsigned)blocks, 128, 0, s>>>(p, lg);
     return cudaGetLastError();
   }
   switch (warps_per_row(p.Bt * p.Dn, p.L)) {
@@ -990,11 +1012,11 @@ cudaError_t bwd_w(const LruBwdParams &q, cudaStream_t s) {
 }
 
 template <typename T, typename Tg> cudaError_t bwd_t(const LruBwdParams &q, cudaStream_t s) {
-  if (const int G = short_lanes(q.f.L)) {
-    const int64_t blocks = (q.f.Bt * q.f.Dn * G + 127) / 128;
+  if (const int lg = short_lanes(q.f.L); lg >= 0) {
+    const int64_t blocks = (((q.f.Bt * q.f.Dn) << lg) + 127) / 128;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const auto kernel = q.f.reset ? lru_bwd_short_kernel<T, Tg, true> : lru_bwd_short_kernel<T, Tg, false>;
-    kernel<<<(unsigned)blocks, 128, 0, s>>>(q, G);
+    kernel<<<(unsigned)blocks, 128, 0, s>>>(q, lg);
     return cudaGetLastError();
   }
   switch (warps_per_row(q.f.Bt * q.f.Dn, q.f.L)) {
@@ -1030,7 +1052,7 @@ cudaError_t launch_lru_bwd(const LruBwdParams &q, int in_bf16, int grad_bf16, cu
   else
     e = grad_bf16 ? bwd_t<float, __nv_bfloat16>(q, s) : bwd_t<float, float>(q, s);
   if (e != cudaSuccess || q.f.Bt == 1 || (!q.dlam && !q.dr_bias && !q.di_bias)) return e;
-  lru_param_sum_kernel<<<(unsigned)((q.f.Dn + 127) / 128), 128, 0, s>>>(q);
+  lru_param_sum_kernel<<<dim3((unsigned)((q.f.Dn + 127) / 128), 3), 128, 0, s>>>(q);
   return cudaGetLastError();
 }
 
