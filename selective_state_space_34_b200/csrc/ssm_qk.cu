@@ -179,7 +179,7 @@ __device__ __forceinline__ void divide(int64_t n, int64_t d, int64_t &q, int64_t
 
 // ---- head elements innermost -------------------------------------------------------------------
 
-// Rows (b, t, h) of one side, heads fastest, walked in steps of dt tokens and dh heads.
+// Rows (b, t, h) of one side, heads fastest, walked one by one.
 struct Walk {
   int64_t token;  // b L + t
   int t, h;
@@ -191,33 +191,26 @@ struct Walk {
     h = (int)hh;
   }
 };
-// A lane's place in one tensor along a walk, moved by additions alone: a step, a step that passes the last head of a
-// token, a step past the last token of a batch element.
+// A lane's place in one tensor along a walk, moved by additions alone: to the next head, past the last head of a token, past
+// the last token of a batch element.
 struct Place {
   int64_t at, step, wrap, turn;
-  __device__ __forceinline__ Place(const QkTensor &x, const Walk &w, int64_t b, int dt, int dh, int H, int L, int o) {
+  __device__ __forceinline__ Place(const QkTensor &x, const Walk &w, int64_t b, int H, int L, int o) {
     at = b * x.sb + w.t * x.sr + w.h * x.sh + o;
-    step = dt * x.sr + dh * x.sh;
+    step = x.sh;
     wrap = x.sr - H * x.sh;
     turn = x.sb - L * x.sr;
   }
 };
-// One step; true where the token changed.
-template <typename... P>
-__device__ __forceinline__ bool advance(Walk &w, int dt, int dh, int H, int L, P &...places) {
-  w.h += dh;
+// One row on; true where the token changed.
+template <typename... P> __device__ __forceinline__ bool advance(Walk &w, int H, int L, P &...places) {
   ((places.at += places.step), ...);
-  if (dt == 0 && w.h < H) return false;  // the common step: another head of the token
-  const bool more = w.h >= H;
-  const int moved = dt + (more ? 1 : 0);
-  w.t += moved;
-  w.token += moved;
-  if (more) {
-    w.h -= H;
-    ((places.at += places.wrap), ...);
-  }
-  while (w.t >= L) {
-    w.t -= L;
+  if (++w.h < H) return false;
+  w.h = 0;
+  w.token++;
+  ((places.at += places.wrap), ...);
+  if (++w.t == L) {
+    w.t = 0;
     ((places.at += places.turn), ...);
   }
   return true;
@@ -232,8 +225,8 @@ template <typename... F> __device__ __forceinline__ void sum_lanes(int G, F &...
   }
 }
 
-// Rows in runs that start at multiples of V elements. CTAs [0, nb0) take the queries, the others the keys; a warp takes `per`
-// consecutive rows of its side, 32 / G at a time (G lanes a row, a unit of up to 16 elements each), and the rows ahead
+// Rows in runs that start at multiples of V elements. CTAs [0, nb0) take the queries, the others the keys; G lanes take `per`
+// consecutive rows of their side, one at a time, a unit of up to 16 elements each, and the rows ahead
 // travel in a ring of cp.async slots that every lane fills, in pieces of V elements, and reads alone. Cosines and sines are
 // recomputed where the token changes; pairs that are not rotated keep 1 and 0. The backward adds its share of dw over all its
 // rows.
@@ -251,10 +244,9 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   const int64_t per = side ? per1 : per0;
   const int H = p.H[side], L = (int)p.L;
   const QkTensor in = p.in[side], dout = p.dout[side], out = p.out[side];
-  const int64_t first = ((int64_t)block * (kThr / 32) + (threadIdx.x >> 5)) * per;
-  const int64_t total = p.Bt * p.L * H;
-  const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
-  const int dt = step / H, dh = step % H;
+  const int64_t total = p.Bt * p.L * H, first = ((int64_t)block * (kThr / 32) + (threadIdx.x >> 5)) * step * per;
+  auto rows_from = [&](int64_t row) { return (int)(row >= total ? 0 : total - row < per ? total - row : per); };
+  const int n_steps = rows_from(first), n_rows = rows_from(first + grp * per);  // of the warp, of this group
   // unit u: two runs, of n1 elements at o1 and n2 at o2. Half layout: the first and the second members of 8 pairs (fewer in the
   // last such unit), then 16 elements a unit behind the rotated part; interleaved: 16 elements a unit.
   const int ur = (p.rot / 2 + 7) / 8, half_rot = p.rot / 2;
@@ -316,10 +308,10 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   };
   Walk ahead, now;
   int64_t b0;
-  ahead.start(first + grp, H, L, b0);
+  ahead.start(first + grp * per, H, L, b0);
   now = ahead;
-  Place from(in, ahead, b0, dt, dh, H, L, o1), dfrom(dout, ahead, b0, dt, dh, H, L, o1), to(out, now, b0, dt, dh, H, L, o1);
-  int left = n_rows - grp;  // rows of this group still to be asked for, times step
+  Place from(in, ahead, b0, H, L, o1), dfrom(dout, ahead, b0, H, L, o1), to(out, now, b0, H, L, o1);
+  int left = n_rows;  // rows still to be asked for
   auto fetch = [&](int stage) {
     if (left > 0) {
       if (reads_v) {
@@ -332,9 +324,9 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
         copy(stage, kSlotsV, a, n1);
         copy(stage, kSlotsV + kSlotsG / 2, a + gap, n2);
       }
-      left -= step;
-      if (BWD) advance(ahead, dt, dh, H, L, from, dfrom);
-      else advance(ahead, dt, dh, H, L, from);
+      left--;
+      if (BWD) advance(ahead, H, L, from, dfrom);
+      else advance(ahead, H, L, from);
     } else {
       clear(stage);  // behind the group's last row: zeros, which add nothing to dw
     }
@@ -371,19 +363,19 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
       store_pieces<float, V>(q + gap, v + 8, n2);
     }
   };
-  // given positions: the next token's is loaded when a token begins, where the walk says which it is
-  const bool known = p.pos && rot && (dt == 0 || dh == 0);
-  int64_t coming = known && grp < n_rows ? position(p, now.token, now.t) : 0;
+  // given positions: the next token's is loaded when a token begins
+  const bool known = p.pos && rot;
+  int64_t coming = known && n_rows ? position(p, now.token, now.t) : 0;
   __syncthreads();
   int stage = 0;
   bool fresh = true;
-  for (int i = 0; i < n_rows; i += step) {
-    const bool live = i + grp < n_rows;
+  for (int i = 0; i < n_steps; i++) {
+    const bool live = i < n_rows;
     fetch(stage == 0 ? S - 1 : stage - 1);
     if (fresh && rot && live) {
       const int64_t pos = known ? coming : position(p, now.token, now.t);
       if (known) {
-        const int64_t token = min(now.token + (dt ? dt : 1), p.Bt * p.L - 1);
+        const int64_t token = min(now.token + 1, p.Bt * p.L - 1);
         coming = position(p, token, 0);
       }
 #pragma unroll
@@ -466,7 +458,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
       if (on && live) store(v1, v2);
     }
     stage = stage == S - 1 ? 0 : stage + 1;
-    fresh = advance(now, dt, dh, H, L, to);
+    fresh = advance(now, H, L, to);
   }
   if constexpr (!BWD) return;
   if (!p.dw[side]) return;
@@ -503,10 +495,9 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
   const int64_t per = side ? per1 : per0;
   const int H = p.H[side], L = (int)p.L;
   const QkTensor in = p.in[side], dout = p.dout[side], out = p.out[side];
-  const int64_t first = ((int64_t)block * (kThr / 32) + (threadIdx.x >> 5)) * per;
-  const int64_t total = p.Bt * p.L * H;
-  const int n_rows = (int)(first >= total ? 0 : total - first < per ? total - first : per);  // of this warp
-  const int dt = step / H, dh = step % H;
+  const int64_t total = p.Bt * p.L * H, first = ((int64_t)block * (kThr / 32) + (threadIdx.x >> 5)) * step * per;
+  auto rows_from = [&](int64_t row) { return (int)(row >= total ? 0 : total - row < per ? total - row : per); };
+  const int n_steps = rows_from(first), n_rows = rows_from(first + grp * per);  // of the warp, of this group
   const bool reads_v = !BWD || p.norm;
   // the lane's units: first run, distance to the second (0: none, at an odd end), weights, sums of dw
   int o[NU], gap[NU];
@@ -528,12 +519,12 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
   }
   Walk ahead, now;
   int64_t b0;
-  ahead.start(first + grp, H, L, b0);
+  ahead.start(first + grp * per, H, L, b0);
   now = ahead;
-  Place from(in, ahead, b0, dt, dh, H, L, 0), dfrom(dout, ahead, b0, dt, dh, H, L, 0), to(out, now, b0, dt, dh, H, L, 0);
+  Place from(in, ahead, b0, H, L, 0), dfrom(dout, ahead, b0, H, L, 0), to(out, now, b0, H, L, 0);
   T nv[NU][2];
   Td ng[NU][2];
-  int left = n_rows - grp;
+  int left = n_rows;  // rows still to be asked for
   auto fetch = [&]() {
     const T *a = static_cast<const T *>(in.p) + from.at;
     const Td *g = static_cast<const Td *>(dout.p) + dfrom.at;
@@ -552,14 +543,14 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
         }
       }
     }
-    left -= step;
-    if (BWD) advance(ahead, dt, dh, H, L, from, dfrom);
-    else advance(ahead, dt, dh, H, L, from);
+    left--;
+    if (BWD) advance(ahead, H, L, from, dfrom);
+    else advance(ahead, H, L, from);
   };
   fetch();
   bool fresh = true;
-  for (int i = 0; i < n_rows; i += step) {
-    const bool live = i + grp < n_rows;
+  for (int i = 0; i < n_steps; i++) {
+    const bool live = i < n_rows;
     float v[NU][2], g[NU][2];
 #pragma unroll
     for (int n = 0; n < NU; n++)
@@ -612,7 +603,7 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
         if (gap[n]) st1(out.p, out.bf16, to.at + o[n] + gap[n], y);
       }
     }
-    fresh = advance(now, dt, dh, H, L, to);
+    fresh = advance(now, H, L, to);
   }
   if constexpr (BWD) {
     if (!p.dw[side]) return;
@@ -1117,7 +1108,10 @@ void split_blocks(const int64_t *work, int64_t most, int *nb0, int *nb1) {
   *nb1 = (int)n[1];
 }
 
-// How the rows of both sides are cut: CTAs of the queries and of both, rows per warp (whole steps of 32 / G rows).
+// How the rows of both sides are cut: CTAs of the queries and of both, rows per group of G lanes: whole tokens where
+// that adds a quarter at most, so that the groups of a warp need their angles at the same steps (2 x 4096 tokens x 40 heads of 128,
+// forward and backward: 88 us so, 95 without); not where rows are copied element by element (fp32, 24 x 197 x 7 heads of 192
+// with 126 turned: 36 us so, 29 without).
 struct RowPlan {
   int V, G, nb0, nb;
   int64_t per[2];
@@ -1136,11 +1130,13 @@ bool plan_rows(const QkParams &p, bool bwd, RowPlan *r) {
   }
   split_blocks(work, most, &n[0], &n[1]);
   for (int j = 0; j < 2; j++) {
-    r->per[j] = step;
+    r->per[j] = 1;
     if (!n[j]) continue;
-    const int64_t warps = (int64_t)n[j] * kWarps, per = (rows[j] + warps - 1) / warps;
-    r->per[j] = (per + step - 1) / step * step;
+    const int64_t groups = (int64_t)n[j] * kWarps * step, per = (rows[j] + groups - 1) / groups;
+    const int64_t whole = (per + p.H[j] - 1) / p.H[j] * p.H[j];
+    r->per[j] = r->V != 1 && (whole - per) * 4 <= per ? whole : per;
     if (r->per[j] > 0x7fffff00) return false;
+    n[j] = (int)((rows[j] + r->per[j] * kWarps * step - 1) / (r->per[j] * kWarps * step));
   }
   r->nb0 = n[0];
   r->nb = n[0] + n[1];
