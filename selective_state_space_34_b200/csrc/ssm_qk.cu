@@ -14,7 +14,7 @@
 // half layout, 16 consecutive ones of the interleaved layout and of the unrotated rest -- so the rotation needs
 // no exchange between lanes. G lanes hold a row (G = units rounded up to a power of two) and add
 // its squares by shuffles. Where runs start at multiples of 4 or 2 elements only, they travel in 8- or 4-byte pieces of the same
-// units; odd head sizes take units of one pair.
+// units; odd head sizes take units of one pair. A group of lanes walks the heads of a token, for their common angles.
 //
 // Time innermost (time_last): a warp owns 32 consecutive steps of 8 or 16 pairs and walks the heads on one set of cosines and
 // sines; a step's squares meet by shuffles, and across the warps of a larger head through shared memory.
@@ -24,10 +24,11 @@
 // the reduced angle, exact but for the frequency's rounding in 64 bits (an angle of x radians is off by about x 2^-53);
 // what is left goes through the hardware sine (absolute error 2^-21) for bf16, sincospif for fp32 inputs.
 //
-// What bounds it. HBM by its bytes; issue in fact (66% and 59% of the slots: 17 a element forwards, 25 backwards, of which the
-// angles are 1 to 6 by the number of heads that share them). 2 x 4096 tokens x 40 heads x 128, bf16: forward 36 us (4.7 TB/s), backward
-// 52 us (4.9 TB/s), with direct loads of four rows a step 64 and 112 us. Time innermost, 8 x 65536 steps x 16 components, queries
-// and keys, forward and backward: 83 us; without the ring, from L1, 116 us.
+// What bounds it. HBM by its bytes; in fact issue and the latency of a row's chain together (60% and 56% of the slots, 13 a element
+// forwards and 23 backwards, of which the angles are 1 to 6 by the number of heads that share them). 2 x 4096 tokens x 40 heads x 128,
+// bf16: forward 34 us (4.9 TB/s), backward 54 us (4.7 TB/s), with direct loads of four rows a step 64 and 112 us. Time innermost,
+// 8 x 65536 steps x 16 components, queries and keys, forward and backward: 75 us, without the ring, from L1, 116 us;
+// 4 x 8192 steps x 3 heads of 128: 61 us, by one warp for all pairs, in two passes from L1, 126 us.
 #include <type_traits>
 
 #include "ssm_internal.h"
@@ -420,7 +421,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
         float sum = s2.x + s2.y, dot = t2.x + t2.y;
         sum_lanes(G, sum, dot);
         const float sc = live ? inv_rms(p, sum) : 0.f;  // with an eps of 0, 1 / sqrt(0) of a row that is none
-        const float2 k2 = splat(-sc * sc * sc * dot * p.inv_D), sc2 = splat(sc);
+        const float2 k2 = splat(-(sc * sc * dot * p.inv_D) * sc), sc2 = splat(sc);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
           d1[j] = fma2(mul2(g1[j], sc2), v1[j], d1[j]);
@@ -677,7 +678,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
   constexpr bool PRECISE = sizeof(T) == 4;
   using Ring = TimeRing<T, Td, BWD, NP, FULL>;
   constexpr int S = Ring::S, kV = Ring::kV, kG = Ring::kG, kMost = NP == 2 ? kThr / 16 : kThr / 32;  // most warps
-  extern __shared__ __align__(16) char smem[];  // the ring, then (warps, 2, D) sums of dw
+  extern __shared__ __align__(16) char smem[];  // the ring, then (groups, 2, D) sums of dw
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane & 3, pl = lane >> 2;
   const int all = p.H[0] + p.H[1];
   const bool sums = BWD && p.norm && (p.dw[0] || p.dw[1]), reads_v = !BWD || p.norm;
@@ -953,7 +954,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
       const float r = now.t0 + step < p.L ? inv_rms(p, sum) : 0.f;  // with an eps of 0, 1 / sqrt(0) of a step that is none
       __syncwarp();  // the head before is done with the factors
       factors[warp][0][step] = r;
-      if (BWD) factors[warp][BWD ? 1 : 0][step] = -r * r * r * dot * p.inv_D;
+      if (BWD) factors[warp][BWD ? 1 : 0][step] = -(r * r * dot * p.inv_D) * r;
       __syncwarp();
 #pragma unroll
       for (int e = 0; e < 4; e++) {
@@ -1188,7 +1189,8 @@ cudaError_t time_ring(const QkParams &p, const TimePlan &plan, int nb, int warps
 
 template <typename T, typename Td, bool BWD> cudaError_t time_run(const QkParams &p, int *nb, cudaStream_t s) {
   const int all = p.H[0] + p.H[1], pairs = pairs_of(p);
-  // one pair a lane where eight warps hold them all, else two, of up to sixteen warps
+  // one pair a lane where eight warps hold them all (4 x 8192 steps x 3 heads of 128, forward and backward: 72 us so, 108 us with two
+  // pairs in half the warps), else two, in up to sixteen warps
   const int NP = pairs <= kThr / 4 ? 1 : 2, warps = pairs <= kThr / 2 ? kThr / 32 : kThr / 16;
   TimePlan t;
   t.W = (pairs + 8 * NP - 1) / (8 * NP);

@@ -131,6 +131,15 @@ def test_rows_off_their_boundaries(L, begin, out):
             assert whole[n][..., :begin].isnan().all() and whole[n][..., begin + L:].isnan().all()
 
 
+@pytest.mark.parametrize("time,D", [(False, 64), (False, 33), (True, 16), (True, 33)])
+def test_rows_of_tiny_values(time, D):
+    """Without an eps the reciprocal of the norm is large: its cube is beyond fp32, the gradients are not."""
+    t = inputs(2, 24, 2, 1, D, F32, time)
+    for n in ("q", "k"):
+        t[n] *= 1e-14
+    run_and_check(t, freq(D // 2 * 2), True, False, time, eps=0.0, grads=(F32,))
+
+
 @pytest.mark.parametrize("time", [False, True])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_rotation_alone(dtype, time):
