@@ -29,7 +29,7 @@
 // rounding into the output's type; sigmoid, exp2 and the root are the hardware's (1 to 4 units of 2^-24), for
 // fp32 inputs too: against float64 the fp32 outputs are off by 2e-7 to 3e-7.
 //
-// What bounds it. HBM, at 80% of the measured copy rate on long rows (bf16, 1 x 5120 x 65536 forward: 500 us, 5.4 TB/s;
+// What bounds it. HBM, at 80% of the measured copy rate on long rows (bf16, 1 x 5120 x 65536 forward: 493 us, 5.4 TB/s;
 // 4 x 4096 x 4096 forward 100 us and backward 165 us of 82 and 143 us): 38 issue slots per element forwards and 58 backwards
 // are 72% and 65% of the SMs' issue, the four MUFU operations per element 60% of theirs forwards. What got it there:
 // packed fp32 pairs (59 -> 43 slots), 32-bit step counts and one branch around whole chunks (43 -> 37; 611 -> 552 us), the
@@ -454,6 +454,8 @@ __global__ void __launch_bounds__(32 * W, W <= 4 ? 28 / W : 1) lru_fwd_kernel(co
 
 // ---- backward ----------------------------------------------------------------------------------
 
+// 16 warps an SM by their registers, of one to sixteen a row. (Eight a row with 138 registers and one CTA an SM: 1 x 256 x 65536
+// forward and backward 123 us, with 128 and two 102 us.)
 template <typename T, typename Tg, int W, bool RESET>
 __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(const __grid_constant__ LruBwdParams q) {
   const LruParams &p = q.f;

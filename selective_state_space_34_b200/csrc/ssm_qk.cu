@@ -1154,8 +1154,8 @@ template <typename K> cudaError_t launch_rows(K kernel, const QkParams &p, const
 }
 
 // Head elements innermost, forward (Td = T) or backward. CTAs: what fits the SMs at once, two each, three where a
-// forward goes by pairs. (Three forward CTAs of runs an SM, which leaves 80 registers and a few spills: 4 x 4096 tokens x 4
-// heads of 64, 8.5 us against 7.7; 2 x 4096 x 40 of 128 alike.)
+// forward goes by pairs. (Three forward CTAs of runs an SM, which leaves 80 registers and a few spills: 4 x 4096 tokens x
+// one query and one key of 128, 8.5 us against 7.7; 2 x 4096 x 40 of 128 alike.)
 template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams &p, RowPlan *r, cudaStream_t s) {
   if (!plan_rows(p, BWD, r)) return cudaErrorInvalidConfiguration;
   const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * (kThr / r->G) * p.D : 0;
