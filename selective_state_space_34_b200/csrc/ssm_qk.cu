@@ -27,8 +27,8 @@
 // What bounds it. HBM by its bytes; in fact issue and the latency of a row's chain together (60% and 56% of the slots, 13 a element
 // forwards and 23 backwards, of which the angles are 1 to 6 by the number of heads that share them). 2 x 4096 tokens x 40 heads x 128,
 // bf16: forward 34 us (4.9 TB/s), backward 54 us (4.7 TB/s), with direct loads of four rows a step 64 and 112 us. Time innermost,
-// 8 x 65536 steps x 16 components, queries and keys, forward and backward: 75 us, without the ring, from L1, 116 us;
-// 4 x 8192 steps x 3 heads of 128: 61 us, by one warp for all pairs, in two passes from L1, 126 us.
+// 8 x 65536 steps x 16 components, queries and keys, forward and backward: 71 us, without the ring, from L1, 116 us;
+// 4 x 8192 steps x 3 heads of 128: 59 us, by one warp for all pairs, in two passes from L1, 126 us.
 #include <type_traits>
 
 #include "ssm_internal.h"
@@ -710,8 +710,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
     j.h = j.chunk * plan.heads;
     j.h_end = min(all, j.h + plan.heads);
   };
-  auto next = [&](Job &j) {
-    if (++j.h < j.h_end) return false;
+  auto next_item = [&](Job &j) {
     j.tt += plan.dtt;
     j.chunk += plan.dchunk;
     j.b += plan.db;
@@ -724,6 +723,10 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
       j.b++;
     }
     open(j);
+  };
+  auto next = [&](Job &j) {
+    if (++j.h < j.h_end) return false;
+    next_item(j);
     return true;
   };
   Job ahead;
@@ -878,6 +881,12 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
       put_run(x.p, x.bf16, i, m, V, v);
     }
   };
+  // the position of this lane's step, an item ahead
+  auto step_position = [&](const Job &j) {
+    const int64_t t = j.t0 + lane;
+    return p.rot && j.on && t < p.L ? position(p, j.b * p.L + t, t) : 0;
+  };
+  int64_t coming = step_position(now);
   int stage = 0, half = 0;
   bool fresh = true;
   while (now.on) {
@@ -885,9 +894,11 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
     const int m = live(now), sd = now.h >= p.H[0], h = now.h - (sd ? p.H[0] : 0);
     if (fresh) {
       __syncwarp();  // the item before is done with the positions
-      const int64_t t = now.t0 + lane;
-      positions[warp][lane] = p.rot && t < p.L ? position(p, now.b * p.L + t, t) : 0;
+      positions[warp][lane] = coming;
       __syncwarp();
+      Job after = now;
+      next_item(after);
+      coming = step_position(after);
 #pragma unroll
       for (int n = 0; n < NP; n++)
         if (u[n].on && u[n].rot) {
@@ -945,6 +956,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * W) : "memory");
         step = lane;
         sum = dot = 0.f;
+#pragma unroll 4
         for (int j = first; j < first + W; j++) {
           sum += shares[half][j][0][lane];
           if (BWD) dot += shares[half][j][BWD ? 1 : 0][lane];
