@@ -154,14 +154,14 @@ template <typename T, int V> __device__ __forceinline__ void store_pieces(T *p, 
 // The first n (2 or 4) bytes of a 4-byte word, 0 in the others.
 __device__ __forceinline__ void cp_async_part(void *dst, const void *src, int n) {
   const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(src), "r"(n));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(src), "r"(n) : "memory");
 }
 template <int N> __device__ __forceinline__ void cp_async_piece(void *dst, const void *src) {
   if constexpr (N == 16) {
     cp_async16(dst, src);
   } else {
     const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(src), "n"(N));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(src), "n"(N) : "memory");
   }
 }
 
