@@ -662,8 +662,14 @@ template <typename T, typename Td, bool BWD, int NP, bool FULL> struct TimeRing 
   static constexpr int kV = sizeof(T) / 2, kG = BWD ? sizeof(Td) / 2 : 0;  // 16-byte slots of a run of 8
   static constexpr int kRuns = 2 * NP * (kV + kG), kFifth = FULL ? 0 : 2 * NP * ((kV == 1) + (kG == 1));
   static constexpr int kSlots = kRuns + (kFifth + 3) / 4, kStageBytes = kSlots * 512;  // of a lane; of a warp
-  static constexpr int S = kStageBytes <= 3 << 10 ? 4 : kStageBytes <= 4 << 10 ? 3 : kStageBytes <= 6 << 10 ? 2 : 1;  // 128 KB
-  static constexpr int kWarpBytes = S * kStageBytes;
+  static constexpr int S = kStageBytes <= 3 << 10 ? 4 : kStageBytes <= 4 << 10 ? 3 : kStageBytes <= 6 << 10 ? 2 : 1;
+  static constexpr int kWarpBytes = S * kStageBytes;  // 12 KB at most
+  static constexpr int kMost = NP == 2 ? kThr / 16 : kThr / 32;  // most warps of a CTA
+  // The most dynamic shared memory of a launch: rings and sums of dw. W warps hold D <= 16 NP W elements, so that the kMost / W groups'
+  // 8 D bytes each are 128 NP a warp at most.
+  static constexpr int kMostBytes = kMost * (kWarpBytes + 128 * NP);
+  static constexpr int kStatic = kMost * 32 * (BWD ? 2 : 1) * 3 * 4 + kMost * (32 + 8 * NP) * 8;  // the kernel's own arrays
+  static_assert(kMostBytes + kStatic <= 227 << 10, "more shared memory than an SM gives a CTA");
 };
 // How the steps are cut: warps a slice of 32, its heads at a time, their chunks, slices of a batch element; and the batch
 // elements, chunks and slices from one item of a group of warps to its next.
@@ -677,7 +683,7 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
   const int W = plan.W;
   constexpr bool PRECISE = sizeof(T) == 4;
   using Ring = TimeRing<T, Td, BWD, NP, FULL>;
-  constexpr int S = Ring::S, kV = Ring::kV, kG = Ring::kG, kMost = NP == 2 ? kThr / 16 : kThr / 32;  // most warps
+  constexpr int S = Ring::S, kV = Ring::kV, kG = Ring::kG, kMost = Ring::kMost;
   extern __shared__ __align__(16) char smem[];  // the ring, then (groups, 2, D) sums of dw
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane & 3, pl = lane >> 2;
   const int all = p.H[0] + p.H[1];
@@ -1156,6 +1162,8 @@ bool plan_rows(const QkParams &p, bool bwd, RowPlan *r) {
   return true;
 }
 
+// smem: the same for every call of a kernel of runs, for the limit is the kernel's and other host threads may be between setting it and
+// their launch; below what needs asking for where rows go by pairs.
 template <typename K> cudaError_t launch_rows(K kernel, const QkParams &p, const RowPlan &r, int smem, cudaStream_t s) {
   if (smem > 40 * 1024) {  // with the kernels' own 4 KB more than the default 48 KB
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1172,8 +1180,8 @@ template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams
   if (!plan_rows(p, BWD, r)) return cudaErrorInvalidConfiguration;
   const int sums = BWD && (p.dw[0] || p.dw[1]) ? (int)sizeof(float) * (kThr / r->G) * p.D : 0;
   constexpr int kSlots = sizeof(T) + (BWD ? sizeof(Td) : 0);
-  constexpr int ring = kThr * 16 * kSlots * kRowStages<T, Td, BWD>;
-  const int smem = sums > ring ? sums : ring;
+  constexpr int smem = kThr * 16 * kSlots * kRowStages<T, Td, BWD>;
+  static_assert(smem >= kThr * 16 * 4, "G lanes hold D <= 16 G elements: the groups' sums are no more than this");
   const bool inter = p.interleaved;
   switch (r->V) {
     case 8: return launch_rows(inter ? qk_rows_kernel<T, Td, BWD, true, 8> : qk_rows_kernel<T, Td, BWD, false, 8>, p, *r, smem, s);
@@ -1191,9 +1199,13 @@ template <typename T, typename Td, bool BWD> cudaError_t rows_run(const QkParams
 template <typename T, typename Td, bool BWD, int NP>
 cudaError_t time_ring(const QkParams &p, const TimePlan &plan, int nb, int warps, int sums, cudaStream_t s) {
   const bool full = p.vec == 8 && p.L % 8 == 0;
+  using Full = TimeRing<T, Td, BWD, NP, true>;
+  using Part = TimeRing<T, Td, BWD, NP, false>;
   const auto kernel = full ? qk_time_ring_kernel<T, Td, BWD, NP, true> : qk_time_ring_kernel<T, Td, BWD, NP, false>;
-  const int smem = warps * (full ? TimeRing<T, Td, BWD, NP, true>::kWarpBytes : TimeRing<T, Td, BWD, NP, false>::kWarpBytes) + sums;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = warps * (full ? Full::kWarpBytes : Part::kWarpBytes) + sums;
+  // The limit belongs to the kernel, not to this launch: always the same one, so that another host thread's call cannot lower it
+  // between here and the launch.
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, full ? Full::kMostBytes : Part::kMostBytes);
   if (e != cudaSuccess) return e;
   kernel<<<nb, 32 * warps, smem, s>>>(p, plan);
   return cudaGetLastError();
