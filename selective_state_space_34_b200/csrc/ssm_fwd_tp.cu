@@ -391,7 +391,8 @@ static cudaError_t launch_tp_t(const FwdParams &p, cudaStream_t stream) {
   auto kern = p.euler ? ssm_fwd_tp_kernel<NPC, Tin, Tout, true> : ssm_fwd_tp_kernel<NPC, Tin, Tout, false>;
   const int NP = (int)((p.N + 1) & ~int64_t(1));
   const size_t smem = TpSmem::bytes(NP);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit is the kernel's, not this launch's: what its largest N (2 NPC) needs, so that another host thread's call cannot lower it
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TpSmem::bytes(2 * NPC));
   if (e != cudaSuccess) return e;
   const int64_t grid = (p.Dn + kTpCh - 1) / kTpCh * p.Bt;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -57,3 +57,42 @@ def test_threads_do_not_fail_each_others_launches(dtype):
         th.join()
     assert not failed
     assert all(torch.equal(out, want) for _, out, want, _ in calls)
+
+
+@pytest.mark.parametrize("sizes", [(3, 16, 8, 12), (20, 64, 33, 48)])
+def test_threads_of_the_chunked_scan(sizes):
+    """The same of the scan's chunked layout, whose shared memory goes by the number of states."""
+    lib, Bt, Dn, L, calls = _abi.load(), 1, 16, 64, []
+    g = torch.Generator().manual_seed(0)
+    n = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    for N in sizes:
+        t = {"x": n(Bt, Dn, L), "dt": n(Bt, Dn, L), "A_log": n(Dn, N), "B": n(Bt, N, L), "C": n(Bt, N, L)}
+        want = ssm.ssm_scan_fwd(*t.values(), scan_form="chunked")
+        out = torch.zeros_like(want)
+        a = _abi.FwdArgs()
+        for k, v in dict(t, out=out).items():
+            setattr(a, k, v.data_ptr())
+        a.Bt, a.Dn, a.N, a.L, a.delta_softplus = Bt, Dn, N, L, 1
+        a.in_dtype = a.out_dtype = _abi.SSM_F32
+        a.scan_form = _abi.SSM_SCAN_CHUNKED
+        calls.append((a, out, want, t))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(j):
+        stream = torch.cuda.Stream()
+        handle, args = ctypes.c_void_p(stream.cuda_stream), ctypes.byref(calls[j][0])
+        for k in range(20000):
+            status = lib.ssm_scan_fwd(args, handle)
+            if status:
+                failed.append((j, k, status, lib.ssm_last_cuda_error()))
+                break
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in range(len(calls))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed
+    assert all(torch.equal(out, want) for _, out, want, _ in calls)
