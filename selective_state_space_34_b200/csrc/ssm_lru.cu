@@ -22,7 +22,8 @@
 // s = 1 - a^2 the gradient of y times y is q = -lambda y (h - b / s): the a^2 / m of d sqrt(1 - a^2) is
 // folded into b / s, and y / s stays finite as a -> 1 (it tends to 1/2).
 //   dx = lambda m g, di~ = lambda b (1 - g), dr~ = q (1 - r), dlam = sum q sigmoid(lam)/softplus(lam)
-// (the kernel carries -q).
+// 1 - r comes from the gate's own exponential: y over the rate would lose it at a gate held open, and be infinite where
+// softplus(lam) is a denormal.
 //
 // Precision. The decay goes through n = 1 - a (a polynomial for small |la|): 1 - a^2 = n + n a keeps its relative
 // precision where a is near 1, which a itself in 32 bits does not. States, sums and gradients are fp32 up to their one
@@ -116,11 +117,12 @@ __device__ __forceinline__ void arguments(const Raw8<float> &raw, const Gate &g,
   for (int j = 0; j < 4; j++) t[j] = fma2(t[j], splat(-kLog2e), splat(g.shift));
   clamp(t);
 }
-// Both sigmoids from -v log2 e, with one reciprocal: 1/((1+eu)(1+ev)); ev = e^-v on the side, with which
-// 1 - sigmoid(v) = ev sigmoid(v).
-__device__ __forceinline__ void sigmoid2(float2 tu, float2 tv, float2 &su, float2 &sv, float2 &ev) {
+// Both sigmoids from -v log2 e, with one reciprocal: 1/((1+eu)(1+ev)); eu and ev are e^-u and e^-v, with which
+// 1 - sigmoid(v) = ev sigmoid(v) keeps its relative precision at a gate held open.
+__device__ __forceinline__ void sigmoid2(float2 tu, float2 tv, float2 &su, float2 &sv, float2 &eu, float2 &ev) {
+  eu = make_float2(ex2_approx(tu.x), ex2_approx(tu.y));
   ev = make_float2(ex2_approx(tv.x), ex2_approx(tv.y));
-  const float2 pu = add2(make_float2(ex2_approx(tu.x), ex2_approx(tu.y)), splat(1.f)), pv = add2(ev, splat(1.f));
+  const float2 pu = add2(eu, splat(1.f)), pv = add2(ev, splat(1.f));
   const float2 d = mul2(pu, pv);
   const float2 inv = make_float2(rcp_approx(d.x), rcp_approx(d.y));
   su = mul2(pv, inv);
@@ -376,8 +378,8 @@ __global__ void __launch_bounds__(32 * W, W <= 4 ? 28 / W : 1) lru_fwd_kernel(co
     auto coefficients = [&](auto near) {
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        float2 ev, sq, is;
-        sigmoid2(r[j], g[j], r[j], g[j], ev);
+        float2 eu, ev, sq, is;
+        sigmoid2(r[j], g[j], r[j], g[j], eu, ev);
         decay<decltype(near)::value>(fma2(r[j], splat(rate), splat(kTiny)), a[j], sq, is);
         bb[j] = mul2(mul2(mul2(sq, is), g[j]), bb[j]);
       }
@@ -506,14 +508,14 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
   fetch_small((rounds - 1) * W + w);
   const Gate gr = gate_of(p.r_bias ? p.r_bias[d] : 0.f), gi = gate_of(p.i_bias ? p.i_bias[d] : 0.f);
   const float lam = p.lam[d];
-  const float rate = decay_rate(p.c, lam), inv_rate = rate > 0.f ? 1.f / rate : 0.f;
+  const float rate = decay_rate(p.c, lam);
   float carry = q.dh_last ? q.dh_last[row] : 0.f;  // mu arriving at the round's last step from behind
   int buf = 0, stage = 0;
   for (int it = rounds - 1; it >= 0; it--, buf ^= 1) {
     const int k = it * W + w;
     const bool in = inside(R, k);
     const int t0 = k * kChunk + 8 * lane - R.f;
-    float2 a[4], y[4], u[4], v[4], z[4], bb[4], dv[4];
+    float2 a[4], y[4], o[4], u[4], v[4], z[4], bb[4], dv[4];
     fetch(k - (S - 1) * W, stage == 0 ? S - 1 : stage - 1);  // into the slots of the round before
     cp_async_wait<S - 1>();
     {
@@ -534,8 +536,9 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
     auto coefficients = [&](auto near) {
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        float2 r, g, ev, sq, is;
-        sigmoid2(y[j], v[j], r, g, ev);
+        float2 r, g, eu, ev, sq, is;
+        sigmoid2(y[j], v[j], r, g, eu, ev);
+        o[j] = mul2(eu, r);                               // 1 - r
         y[j] = fma2(r, splat(rate), splat(kTiny));
         decay<decltype(near)::value>(y[j], a[j], sq, is);
         u[j] = mul2(mul2(sq, is), g);                     // m g
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
       for (int e = 0; e < 8; e++)
         if (t0 + e < 0 || t0 + e >= R.len) {
           elem(a, e) = 1.f;
-          elem(bb, e) = elem(y, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+          elem(bb, e) = elem(y, e) = elem(o, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
         }
     }
     // the states' maps forwards, and mu -> S mu + M of what leaves the lane's first step backwards
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       h = RESET && cuts ? after2<true>(a[j], h, bb[j]) : fma2(a[j], h, bb[j]);
-      z[j] = fma2(z[j], splat(-1.f), mul2(y[j], h));  // y (h - b / s)
+      z[j] = fma2(mul2(y[j], h), splat(-1.f), z[j]);  // -y (h - b / s)
     }
 #pragma unroll
     for (int j = 3; j >= 0; j--) {
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
       u[j] = mul2(u[j], lm);
       v[j] = mul2(v[j], lm);
       bb[j] = mul2(z[j], lm);
-      z[j] = mul2(bb[j], fma2(y[j], splat(inv_rate), splat(-1.f)));  // -(1 - r) = y / rate - 1
+      z[j] = mul2(bb[j], o[j]);
     }
     if (W == 1) carry = __shfl_sync(kFull, mu.x, 0);
     if (k >= n_ck) continue;
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
   }
   // sigmoid / softplus: 1 as lam -> -inf, where softplus reaches 0
   const float sp = softplus<true>(lam);
-  if (q.p_dlam) q.p_dlam[row] = -sq * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
+  if (q.p_dlam) q.p_dlam[row] = sq * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
   if (q.p_dr) q.p_dr[row] = sr;
   if (q.p_di) q.p_di[row] = si;
 }
@@ -720,8 +723,8 @@ __global__ void __launch_bounds__(128) lru_fwd_short_kernel(const __grid_constan
   pairs(rx, bb);
 #pragma unroll
   for (int j = 0; j < 4; j++) {
-    float2 ev, sq, is;
-    sigmoid2(r[j], g[j], r[j], g[j], ev);
+    float2 eu, ev, sq, is;
+    sigmoid2(r[j], g[j], r[j], g[j], eu, ev);
     decay<false>(fma2(r[j], splat(rate), splat(kTiny)), a[j], sq, is);
     bb[j] = mul2(mul2(mul2(sq, is), g[j]), bb[j]);
   }
@@ -778,17 +781,18 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
   const uint64_t cut = RESET ? load_resets(p, b, R, t0) : 0;
   const Gate gr = gate_of(p.r_bias ? p.r_bias[d] : 0.f), gi = gate_of(p.i_bias ? p.i_bias[d] : 0.f);
   const float lam = p.lam[d];
-  const float rate = decay_rate(p.c, lam), inv_rate = rate > 0.f ? 1.f / rate : 0.f;
+  const float rate = decay_rate(p.c, lam);
   const float hin = p.states[row * p.n_states], behind = q.dh_last ? q.dh_last[row] : 0.f;
-  float2 a[4], y[4], u[4], v[4], z[4], bb[4], dv[4];
+  float2 a[4], y[4], o[4], u[4], v[4], z[4], bb[4], dv[4];
   arguments(rr, gr, y);
   arguments(ri, gi, v);
   pairs(rx, bb);
   pairs(rd, dv);
 #pragma unroll
   for (int j = 0; j < 4; j++) {
-    float2 rg, g, ev, sq, is;
-    sigmoid2(y[j], v[j], rg, g, ev);
+    float2 rg, g, eu, ev, sq, is;
+    sigmoid2(y[j], v[j], rg, g, eu, ev);
+    o[j] = mul2(eu, rg);
     y[j] = fma2(rg, splat(rate), splat(kTiny));
     decay<false>(y[j], a[j], sq, is);
     u[j] = mul2(mul2(sq, is), g);
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
     for (int e = 0; e < 8; e++)
       if (t0 + e < 0 || t0 + e >= R.len) {
         elem(a, e) = 1.f;
-        elem(bb, e) = elem(y, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+        elem(bb, e) = elem(y, e) = elem(o, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
       }
   }
   if (RESET && cut) {
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     h = after2<RESET>(a[j], h, bb[j]);
-    z[j] = fma2(z[j], splat(-1.f), mul2(y[j], h));  // y (h - b / s)
+    z[j] = fma2(mul2(y[j], h), splat(-1.f), z[j]);  // -y (h - b / s)
   }
 #pragma unroll
   for (int j = 3; j >= 0; j--) {
@@ -839,7 +843,7 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
     u[j] = mul2(u[j], lm);
     v[j] = mul2(v[j], lm);
     bb[j] = mul2(z[j], lm);
-    z[j] = mul2(bb[j], fma2(y[j], splat(inv_rate), splat(-1.f)));
+    z[j] = mul2(bb[j], o[j]);
   }
   if (!in) {  // steps outside the row hold 0 (0 times an infinite lambda would not be)
 #pragma unroll
@@ -866,7 +870,7 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
   if (gl) return;
   if (q.dh0) q.dh0[row] = mu.x;
   const float sp = softplus<true>(lam);
-  if (q.p_dlam) q.p_dlam[row] = -sq * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
+  if (q.p_dlam) q.p_dlam[row] = sq * (sp > 0.f ? sigmoid<true>(lam) / sp : 1.f);
   if (q.p_dr) q.p_dr[row] = sr;
   if (q.p_di) q.p_di[row] = si;
 }
@@ -923,8 +927,8 @@ __global__ void __launch_bounds__(128) lru_step_kernel(const __grid_constant__ L
     const int f = V == 1 ? e : e + 1;
     float2 t = fma2(make_float2(to_f32(r[e]), to_f32(r[f])), splat(-kLog2e), mul2(make_float2(rb[e], rb[f]), splat(-kLog2e)));
     float2 n = fma2(make_float2(to_f32(g[e]), to_f32(g[f])), splat(-kLog2e), mul2(make_float2(ib[e], ib[f]), splat(-kLog2e)));
-    float2 rr, gg, ev, a, s, is;
-    sigmoid2(make_float2(min_nan(t.x, 60.f), min_nan(t.y, 60.f)), make_float2(min_nan(n.x, 60.f), min_nan(n.y, 60.f)), rr, gg, ev);
+    float2 rr, gg, eu, ev, a, s, is;
+    sigmoid2(make_float2(min_nan(t.x, 60.f), min_nan(t.y, 60.f)), make_float2(min_nan(n.x, 60.f), min_nan(n.y, 60.f)), rr, gg, eu, ev);
     decay<false>(fma2(make_float2(decay_rate(p.c, lam[e]), decay_rate(p.c, lam[f])), rr, splat(kTiny)), a, s, is);
     const float2 in = mul2(mul2(mul2(s, is), gg), make_float2(to_f32(x[e]), to_f32(x[f])));
     const float2 hn = fma2(a, make_float2(h[e], h[f]), in);
