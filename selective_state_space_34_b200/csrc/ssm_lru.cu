@@ -18,9 +18,10 @@
 //
 // Backward. lambda_t = dout_t + a_{t+1} lambda_{t+1} runs from the end over the same chunks with
 // mu_t = a_t (dout_t + mu_{t+1}), an affine map of what arrives from behind; the states come from the
-// state that entered each chunk (saved by the forward) and a second composition. With y = -la and
-// s = 1 - a^2 the gradient of y times y is q = -lambda y (h - b / s): the a^2 / m of d sqrt(1 - a^2) is
-// folded into b / s, and y / s stays finite as a -> 1 (it tends to 1/2).
+// state that entered each chunk (saved by the forward) and a second composition. With y = -la, w = y a and
+// s = 1 - a^2 the gradient of y times y is q = -lambda w (h_{t-1} - a b / s): y / s stays finite as a -> 1 (it
+// tends to 1/2), and neither term holds what the other cancels as a -> 0 (y (h_t - b / s), one instruction a pair shorter, left
+// the rounding of y b in results of the size of y a).
 //   dx = lambda m g, di~ = lambda b (1 - g), dr~ = q (1 - r), dlam = sum q sigmoid(lam)/softplus(lam)
 // 1 - r comes from the gate's own exponential: y over the rate would lose it at a gate held open, and be infinite where
 // softplus(lam) is a denormal.
@@ -515,13 +516,13 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
     const int k = it * W + w;
     const bool in = inside(R, k);
     const int t0 = k * kChunk + 8 * lane - R.f;
-    float2 a[4], y[4], o[4], u[4], v[4], z[4], bb[4], dv[4];
+    float2 a[4], ya[4], o[4], u[4], v[4], z[4], bb[4], dv[4];
     fetch(k - (S - 1) * W, stage == 0 ? S - 1 : stage - 1);  // into the slots of the round before
     cp_async_wait<S - 1>();
     {
       Raw8<T> raw;
       ring.get(stage, 1, raw);
-      arguments(raw, gr, y);
+      arguments(raw, gr, ya);
       ring.get(stage, 2, raw);
       arguments(raw, gi, v);
       ring.get(stage, 0, raw);
@@ -537,14 +538,15 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         float2 r, g, eu, ev, sq, is;
-        sigmoid2(y[j], v[j], r, g, eu, ev);
+        sigmoid2(ya[j], v[j], r, g, eu, ev);
         o[j] = mul2(eu, r);                               // 1 - r
-        y[j] = fma2(r, splat(rate), splat(kTiny));
-        decay<decltype(near)::value>(y[j], a[j], sq, is);
+        const float2 y = fma2(r, splat(rate), splat(kTiny));
+        decay<decltype(near)::value>(y, a[j], sq, is);
+        ya[j] = mul2(y, a[j]);
         u[j] = mul2(mul2(sq, is), g);                     // m g
         bb[j] = mul2(bb[j], u[j]);                        // m g x
         v[j] = mul2(bb[j], mul2(ev, g));                  // b (1 - g)
-        z[j] = mul2(mul2(mul2(y[j], is), is), bb[j]);     // y b / s
+        z[j] = mul2(mul2(mul2(mul2(ya[j], is), is), a[j]), bb[j]);  // y a^2 b / s
       }
     };
     if (rate < kNear) coefficients(std::true_type());
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
       for (int e = 0; e < 8; e++)
         if (t0 + e < 0 || t0 + e >= R.len) {
           elem(a, e) = 1.f;
-          elem(bb, e) = elem(y, e) = elem(o, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+          elem(bb, e) = elem(ya, e) = elem(o, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
         }
     }
     // the states' maps forwards, and mu -> S mu + M of what leaves the lane's first step backwards
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
     if (cuts) {
 #pragma unroll
       for (int e = 0; e < 8; e++)
-        if (cut >> (8 * e) & 0xff) elem(a, e) = 0.f;
+        if (cut >> (8 * e) & 0xff) elem(a, e) = elem(ya, e) = 0.f;
       compose<true>(a, bb, P2, H2);
       // a cut stops mu whatever the other factors are (NaN, in a sequence of its own)
       const float Sx = cut & 0xffffffffu ? 0.f : P2.x, Sy = cut >> 32 ? 0.f : P2.y;
@@ -610,9 +612,9 @@ __global__ void __launch_bounds__(32 * W, W <= 8 ? 16 / W : 1) lru_bwd_kernel(co
     mu.y = lane == 31 ? into : after<RESET>(Se, into, Me);
     mu.x = after<RESET>(P2.y, mu.y, M2.y);
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < 4; j++) {  // -y (a h_{t-1} - a^2 b / s)
+      z[j] = fma2(RESET && cuts ? after2<true>(ya[j], h, splat(0.f)) : mul2(ya[j], h), splat(-1.f), z[j]);
       h = RESET && cuts ? after2<true>(a[j], h, bb[j]) : fma2(a[j], h, bb[j]);
-      z[j] = fma2(mul2(y[j], h), splat(-1.f), z[j]);  // -y (h - b / s)
     }
 #pragma unroll
     for (int j = 3; j >= 0; j--) {
@@ -783,22 +785,23 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
   const float lam = p.lam[d];
   const float rate = decay_rate(p.c, lam);
   const float hin = p.states[row * p.n_states], behind = q.dh_last ? q.dh_last[row] : 0.f;
-  float2 a[4], y[4], o[4], u[4], v[4], z[4], bb[4], dv[4];
-  arguments(rr, gr, y);
+  float2 a[4], ya[4], o[4], u[4], v[4], z[4], bb[4], dv[4];
+  arguments(rr, gr, ya);
   arguments(ri, gi, v);
   pairs(rx, bb);
   pairs(rd, dv);
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     float2 rg, g, eu, ev, sq, is;
-    sigmoid2(y[j], v[j], rg, g, eu, ev);
+    sigmoid2(ya[j], v[j], rg, g, eu, ev);
     o[j] = mul2(eu, rg);
-    y[j] = fma2(rg, splat(rate), splat(kTiny));
-    decay<false>(y[j], a[j], sq, is);
+    const float2 y = fma2(rg, splat(rate), splat(kTiny));
+    decay<false>(y, a[j], sq, is);
+    ya[j] = mul2(y, a[j]);
     u[j] = mul2(mul2(sq, is), g);
     bb[j] = mul2(bb[j], u[j]);
     v[j] = mul2(bb[j], mul2(ev, g));
-    z[j] = mul2(mul2(mul2(y[j], is), is), bb[j]);
+    z[j] = mul2(mul2(mul2(mul2(ya[j], is), is), a[j]), bb[j]);
   }
   const bool in = t0 >= 0 && t0 + 8 <= R.len;
   if (!in) {
@@ -806,13 +809,13 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
     for (int e = 0; e < 8; e++)
       if (t0 + e < 0 || t0 + e >= R.len) {
         elem(a, e) = 1.f;
-        elem(bb, e) = elem(y, e) = elem(o, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
+        elem(bb, e) = elem(ya, e) = elem(o, e) = elem(u, e) = elem(v, e) = elem(z, e) = elem(dv, e) = 0.f;
       }
   }
   if (RESET && cut) {
 #pragma unroll
     for (int e = 0; e < 8; e++)
-      if (cut >> (8 * e) & 0xff) elem(a, e) = 0.f;
+      if (cut >> (8 * e) & 0xff) elem(a, e) = elem(ya, e) = 0.f;
   }
   float2 P2, H2, M2 = splat(0.f);
   compose<RESET>(a, bb, P2, H2);
@@ -833,8 +836,8 @@ __global__ void __launch_bounds__(128) lru_bwd_short_kernel(const __grid_constan
   mu.x = after<RESET>(Sy, mu.y, M2.y);
 #pragma unroll
   for (int j = 0; j < 4; j++) {
+    z[j] = fma2(after2<RESET>(ya[j], h, splat(0.f)), splat(-1.f), z[j]);  // -y (a h_{t-1} - a^2 b / s)
     h = after2<RESET>(a[j], h, bb[j]);
-    z[j] = fma2(mul2(y[j], h), splat(-1.f), z[j]);  // -y (h - b / s)
   }
 #pragma unroll
   for (int j = 3; j >= 0; j--) {

@@ -51,3 +51,15 @@ def test_gates_held_open(Bt, Dn, L, bias, dtype):
     t["r_bias"], t["i_bias"] = t["r_bias"] + bias, t["i_bias"] + bias
     t["lam"] = torch.linspace(-7.0, -4.0, Dn).cuda()
     run_and_check(t, ("r_bias", "i_bias", "h0"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("Bt,Dn,L", SIZES)
+def test_channels_that_forget_at_once(Bt, Dn, L, packed, dtype):
+    """Decays from 0.6 down to e^-60 a step, some gates open: what is left of the gradient of the decay is of the size of the decay
+    itself, not of the input's rounding."""
+    t = inputs(Bt, Dn, L, dtype, seed=L + 1)
+    t["lam"] = torch.linspace(-3.0, 7.5, Dn).cuda()
+    t["r_bias"] = torch.linspace(-2.0, 4.0, Dn).flip(0).roll(Dn // 3).cuda()
+    run_and_check(t, ("r_bias", "i_bias", "h0") + (("reset", "lengths") if packed else ()))
