@@ -84,17 +84,17 @@ __device__ __forceinline__ void in_order(const float2 *v, float *o) {
   for (int j = 0; j < 4; j++) o[j] = v[j].x, o[4 + j] = v[j].y;
 }
 
-// What a row's gates need of its parameters. A gate's argument is kept above -42 (its sigmoid above 2^-60), so
+// What a row's gates need of its parameters. A gate's argument is kept above -44 (its sigmoid above 2^-63), so
 // that the product of two denominators 1 + e^-v stays finite; NaN passes. bf16 inputs are clamped as they are, two
-// at a time, to `low`, which rounding to bf16 moves by 2 at most while the bias is within 1024; a row with
-// a larger one (a gate held shut or open) clamps the arguments themselves, as fp32 inputs do.
+// at a time, to `low`, which rounding to bf16 moves by 2 at most while the bias is within 960 (`low` then within 1024); a row
+// with a larger one (a gate held shut or open) clamps the arguments themselves, at -41.6, as fp32 inputs do.
 struct Gate {
   float shift;         // -bias log2 e
   __nv_bfloat162 low;  // -41.5 - bias
   bool wide;
 };
 __device__ __forceinline__ Gate gate_of(float bias) {
-  return {-bias * kLog2e, __float2bfloat162_rn(-41.5f - bias), !(fabsf(bias) <= 1024.f)};
+  return {-bias * kLog2e, __float2bfloat162_rn(-41.5f - bias), !(fabsf(bias) <= 960.f)};
 }
 __device__ __forceinline__ void clamp(float2 *t) {
 #pragma unroll

@@ -1,9 +1,11 @@
 """What the kernels' sources have to hold and no run shows."""
 import glob
+import math
 import os
 import re
 
 import pytest
+import torch
 
 from selective_state_space_34_b200 import build
 
@@ -30,3 +32,14 @@ def test_copies_and_waits_order_memory(what):
     assert found
     bad = ["%s: %s" % (f, " ".join(s.split())) for f, s in found if '"memory"' not in s]
     assert not bad, "\n".join(bad)
+
+
+def test_clamped_gates_have_finite_denominators():
+    """bf16 gates are clamped to -41.5 - bias rounded to bf16: up to the bias from which the arguments themselves are clamped, the product of two
+    denominators 1 + e^-v stays below the largest fp32 value."""
+    with open(os.path.join(build.CSRC, "ssm_lru.cu")) as f:
+        limit = float(re.search(r"!\(fabsf\(bias\) <= ([0-9.]+)f\)", f.read()).group(1))
+    bias = torch.arange(-limit, limit + 0.125, 0.125, dtype=torch.float32)
+    low = (-41.5 - bias).to(torch.bfloat16)
+    worst = float((low.double() + bias.double()).min())
+    assert worst >= -44.0 and 2 * math.log2(1 + math.exp(-worst)) < 127.9
