@@ -1084,8 +1084,9 @@ int pow2_at_least(int n) {
 // Pair units of a row.
 int pairs_of(const QkParams &p) { return p.rot / 2 + (p.D - p.rot + 1) / 2; }
 
-// The most elements (8, 4, 2; 1 of fp32) that every run of a row starts at multiples of, and the strides and addresses of both
-// sides are; 0 where a row does not make such runs or more units than a warp has lanes.
+// The most elements (8, 4, 2; 1 of fp32) that every run of a row starts at multiples of, and the addresses and strides of both
+// sides are (those of axes that are stepped along: one of length 1 may have any); 0 where a row does not make such runs or more units
+// than a warp has lanes.
 int run_of(const QkParams &p) {
   const int units = p.interleaved ? (p.D + 15) / 16 : (p.rot / 2 + 7) / 8 + (p.D - p.rot + 15) / 16;
   if (units > 32) return 0;
@@ -1100,7 +1101,9 @@ int run_of(const QkParams &p) {
       if (p.H[s] == 0) continue;
       for (const QkTensor *t : {&p.in[s], &p.out[s], &p.dout[s]}) {
         const int bytes = V * (t->bf16 ? 2 : 4) < 16 ? V * (t->bf16 ? 2 : 4) : 16;
-        if (t->p && (reinterpret_cast<uintptr_t>(t->p) % bytes || t->sb % V || t->sh % V || t->sr % V)) fits = false;
+        if (t->p && (reinterpret_cast<uintptr_t>(t->p) % bytes || (p.Bt > 1 && t->sb % V) || (p.H[s] > 1 && t->sh % V) ||
+                     (p.L > 1 && t->sr % V)))
+          fits = false;
       }
     }
     if (fits) return V;
