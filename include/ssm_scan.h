@@ -497,7 +497,7 @@ typedef struct ssm_qk_args {
   int64_t Bt, L, Hq, Hk, D;
   int64_t rot;             /* rotated elements: even, 0 .. D */
   int64_t pos0;
-  float eps, rot_scale;    /* eps >= 0 */
+  float eps, rot_scale;    /* eps >= 0; below 2^-126 it counts as 2^-126: a row of zeros gives zeros */
   int32_t layout;          /* ssm_qk_layout */
   int32_t norm, interleaved, freq_f64, pos_i64;
   int32_t in_dtype, out_dtype;

@@ -2,6 +2,7 @@
 // rotation of queries and keys, and of the state-space-dual step: host-side validation (synchronous,
 // before any launch), workspace carving, dispatch. No exception crosses the ABI, no device memory
 // is allocated.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -191,7 +192,8 @@ ssm::QkParams qk_params(const ssm_qk_args *a) {
   p.interleaved = a->interleaved != 0;
   p.norm = a->norm != 0;
   p.time_last = a->layout == SSM_QK_TIME_LAST;
-  p.eps = a->eps;
+  // a reciprocal root of 2^63 at most: its square is finite in fp32, and a subnormal mean square never stands alone under a root that flushes it
+  p.eps = a->eps > FLT_MIN ? a->eps : FLT_MIN;
   p.rot_scale = a->rot_scale;
   p.inv_D = 1.f / (float)a->D;
   return p;

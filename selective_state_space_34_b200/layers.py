@@ -110,8 +110,8 @@ def ssm_qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, inv_freq=None,
     innermost as the selective scan's B and C are (C.unsqueeze(1) is one head). Any strides but a dense last axis:
     slices of one projection need no copy. ``inv_freq`` ((rot / 2,) fp32 or fp64, see ssm_rope_inv_freq): the
     first rot elements of a head turn by position * inv_freq[j] in pairs (j, j + rot / 2), or (2 j, 2 j + 1) with
-    ``interleaved``; cosine and sine are multiplied by ``rot_scale``. ``positions``: (Bt, L) int32 or int64, or None
-    for pos0 + t. ``out``: (q_out, k_out) to write to, possibly q and k themselves (None in a place:
+    ``interleaved``; cosine and sine are multiplied by ``rot_scale``. An ``eps`` below 2^-126 counts as 2^-126. ``positions``:
+    (Bt, L) int32 or int64, or None for pos0 + t. ``out``: (q_out, k_out) to write to, possibly q and k themselves (None in a place:
     allocated). Returns (q_out, k_out)."""
     q_out, k_out = (None, None) if out is None else out
     return _abi.marshal().qk_fwd(q, k, q_weight, k_weight, inv_freq, positions, pos0, norm, eps, interleaved, rot_scale,

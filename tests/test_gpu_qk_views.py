@@ -37,3 +37,23 @@ def test_strides_of_axes_of_length_one_do_not_matter(axis, D):
     g = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], **kw)
     h = ssm.ssm_qk_norm_rope_bwd(view(t["dq_out"]), view(t["q"]), **kw)
     assert all(torch.equal(g[n], h[n]) for n in g)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("time,D", [(False, 64), (False, 33), (False, 80), (True, 16), (True, 33), (True, 200)])
+def test_rows_whose_squares_are_subnormal(time, D, dtype):
+    """An eps of 0 counts as 2^-126: rows of 1e-20 and of zeros have finite results and gradients, those of the formula with that eps.
+    (Squares of 1e-40 are off by 2^-150 each and in their sum: 2^-23 of an eps of 2^-126, inside the bounds' 64 and 128 EPS.)"""
+    t = inputs(2, 24, 2, 1, D, dtype, time, seed=D)
+    for n in ("q", "k"):
+        t[n] = (t[n].float() * 1e-20).to(dtype)
+        ref.qk_rows(t[n], time)[:, 3] = 0.0
+    f = freq(D // 2 * 2)
+    kw = dict(q_weight=t["q_weight"], k_weight=t["k_weight"], inv_freq=f, positions=t["positions"], layout="bhdl" if time else "blhd")
+    out = ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], out_dtype=F32, eps=0.0, **kw)
+    g = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], t["dk_out"], t["k"], eps=0.0, **kw)
+    for side, o in zip("qk", out):
+        want = ref.qk(t[side], t[side + "_weight"], f, t["positions"], True, 2.0 ** -126, False, 1.0, time, t["d%s_out" % side])
+        for name, got, (v, b) in ((side + "_out", o, want["out"]), ("d" + side, g["d" + side], want["d"]),
+                                  ("d%s_weight" % side, g["d%s_weight" % side], want["dw"])):
+            ref.check(name, got, v, b + ref.EPS * v.abs() + 1e-37)
