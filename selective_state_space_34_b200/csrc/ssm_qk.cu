@@ -55,17 +55,22 @@ __device__ __forceinline__ int64_t position(const QkParams &p, int64_t token, in
   if (!p.pos) return p.pos0 + t;
   return p.pos_i64 ? static_cast<const int64_t *>(p.pos)[token] : (int64_t)static_cast<const int32_t *>(p.pos)[token];
 }
-// Turns per position of pair j, in units of 2^-64 turns modulo 1.
-__device__ __forceinline__ uint64_t frequency(const QkParams &p, int j) {
+// Turns per position of a pair, in units of 2^-64 turns modulo 1, and the factor on its cosine and sine: the call's, or NaN where the
+// frequency is NaN or infinite, which the integer cannot say.
+struct alignas(16) Rate {
+  uint64_t turns;
+  float scale;
+};
+__device__ __forceinline__ Rate rate_of(const QkParams &p, int j) {
   const double f = kInvTwoPi *
                    (p.freq_f64 ? static_cast<const double *>(p.inv_freq)[j] : (double)static_cast<const float *>(p.inv_freq)[j]);
-  return (uint64_t)((f - floor(f)) * 18446744073709551616.0);
+  if (!isfinite(f)) return {0, __int_as_float(0x7fffffff)};
+  return {(uint64_t)((f - floor(f)) * 18446744073709551616.0), p.rot_scale};
 }
-// Cosine and sine of pos * f turns, times the scale. The product modulo 2^64 is the angle's fraction of a turn, whatever the
+// Cosine and sine of pos turns of a pair, times the factor. The product modulo 2^64 is the angle's fraction of a turn, whatever the
 // position and its sign.
-template <bool PRECISE>
-__device__ __forceinline__ void turn(int64_t pos, uint64_t f, float scale, float &c, float &s) {
-  const float frac = (float)(int32_t)(((uint64_t)pos * f) >> 32);  // in 2^-32 turns, from -1/2 to 1/2
+template <bool PRECISE> __device__ __forceinline__ void turn(int64_t pos, const Rate &r, float &c, float &s) {
+  const float frac = (float)(int32_t)(((uint64_t)pos * r.turns) >> 32);  // in 2^-32 turns, from -1/2 to 1/2
   if (PRECISE) {
     sincospif(frac * 0x1p-31f, &s, &c);
   } else {
@@ -73,8 +78,8 @@ __device__ __forceinline__ void turn(int64_t pos, uint64_t f, float scale, float
     c = __cosf(x);
     s = __sinf(x);
   }
-  c *= scale;
-  s *= scale;
+  c *= r.scale;
+  s *= r.scale;
 }
 __device__ __forceinline__ float inv_rms(const QkParams &p, float sum) {
   float r;  // 2^-23 of the result at most
@@ -270,7 +275,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
   constexpr bool kAll = !INTER && V == 8;  // all 8 of a rotated unit (the half layout's run starts are then multiples of 8)
   // in shared memory, by unit: the weights of its pairs' members, and its pairs' turns per position
   __shared__ float4 sw[4][32];
-  __shared__ uint64_t sf[8][32];
+  __shared__ Rate sf[8][32];
   for (int j = threadIdx.x; j < 16 * G; j += kThr) {  // lanes without a unit read weights too: 1, which their zeros stay 0 with
     const int u = j >> 4, e = j & 15;
     int a1, a2, m1, m2;
@@ -280,7 +285,7 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
     const int k = INTER ? (e & 1) * 8 + e / 2 : e;  // first members of the 8 pairs, then second ones
     reinterpret_cast<float *>(&sw[k >> 2][u])[k & 3] = has ? p.w[side][at] : 1.f;
   }
-  for (int j = threadIdx.x; j < p.rot / 2; j += kThr) sf[j & 7][j >> 3] = frequency(p, j);
+  for (int j = threadIdx.x; j < p.rot / 2; j += kThr) sf[j & 7][j >> 3] = rate_of(p, j);
   float2 d1[4], d2[4], c[4], s[4];
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -381,8 +386,8 @@ qk_rows_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0,
       }
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        if (kAll || 2 * j < turned) turn<PRECISE>(pos, sf[2 * j][sub], p.rot_scale, c[j].x, s[j].x);
-        if (kAll || 2 * j + 1 < turned) turn<PRECISE>(pos, sf[2 * j + 1][sub], p.rot_scale, c[j].y, s[j].y);
+        if (kAll || 2 * j < turned) turn<PRECISE>(pos, sf[2 * j][sub], c[j].x, s[j].x);
+        if (kAll || 2 * j + 1 < turned) turn<PRECISE>(pos, sf[2 * j + 1][sub], c[j].y, s[j].y);
       }
     }
     cp_async_wait<S - 1>();
@@ -565,7 +570,7 @@ qk_pairs_kernel(const __grid_constant__ QkParams p, int G, int nb0, int64_t per0
       const int64_t pos = position(p, now.token, now.t);
 #pragma unroll
       for (int n = 0; n < NU; n++)
-        if (rot[n]) turn<PRECISE>(pos, frequency(p, sub + n * G), p.rot_scale, c[n], s[n]);
+        if (rot[n]) turn<PRECISE>(pos, rate_of(p, sub + n * G), c[n], s[n]);
     }
     float sum = 0.f, dot = 0.f;
 #pragma unroll
@@ -668,7 +673,7 @@ template <typename T, typename Td, bool BWD, int NP, bool FULL> struct TimeRing 
   // The most dynamic shared memory of a launch: rings and sums of dw. W warps hold D <= 16 NP W elements, so that the kMost / W groups'
   // 8 D bytes each are 128 NP a warp at most.
   static constexpr int kMostBytes = kMost * (kWarpBytes + 128 * NP);
-  static constexpr int kStatic = kMost * 32 * (BWD ? 2 : 1) * 3 * 4 + kMost * (32 + 8 * NP) * 8;  // the kernel's own arrays
+  static constexpr int kStatic = kMost * 32 * (BWD ? 2 : 1) * 3 * 4 + kMost * (32 + 16 * NP) * 8;  // the kernel's own arrays
   static_assert(kMostBytes + kStatic <= 227 << 10, "more shared memory than an SM gives a CTA");
 };
 // How the steps are cut: warps a slice of 32, its heads at a time, their chunks, slices of a batch element; and the batch
@@ -848,11 +853,11 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
   };
 #pragma unroll
   for (int j = 0; j < S - 1; j++) fetch(j);
-  __shared__ uint64_t freq[kMost][NP][8];  // by pair
+  __shared__ Rate freq[kMost][NP][8];  // by pair
   float2 cs[NP][4], sn[NP][4];
 #pragma unroll
   for (int n = 0; n < NP; n++) {
-    if (tl == 0 && u[n].on && u[n].rot) freq[warp][n][pl] = frequency(p, pl + 8 * (warp - first + n * W));
+    if (tl == 0 && u[n].on && u[n].rot) freq[warp][n][pl] = rate_of(p, pl + 8 * (warp - first + n * W));
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       cs[n][e] = splat(1.f);
@@ -908,11 +913,11 @@ qk_time_ring_kernel(const __grid_constant__ QkParams p, const __grid_constant__ 
 #pragma unroll
       for (int n = 0; n < NP; n++)
         if (u[n].on && u[n].rot) {
-          const uint64_t f = freq[warp][n][pl];
+          const Rate f = freq[warp][n][pl];
 #pragma unroll
           for (int e = 0; e < 4; e++) {
-            turn<PRECISE>(positions[warp][8 * tl + 2 * e], f, p.rot_scale, cs[n][e].x, sn[n][e].x);
-            turn<PRECISE>(positions[warp][8 * tl + 2 * e + 1], f, p.rot_scale, cs[n][e].y, sn[n][e].y);
+            turn<PRECISE>(positions[warp][8 * tl + 2 * e], f, cs[n][e].x, sn[n][e].x);
+            turn<PRECISE>(positions[warp][8 * tl + 2 * e + 1], f, cs[n][e].y, sn[n][e].y);
           }
         }
     }
@@ -1168,7 +1173,7 @@ bool plan_rows(const QkParams &p, bool bwd, RowPlan *r) {
 // smem: the same for every call of a kernel of runs, for the limit is the kernel's and other host threads may be between setting it and
 // their launch; below what needs asking for where rows go by pairs.
 template <typename K> cudaError_t launch_rows(K kernel, const QkParams &p, const RowPlan &r, int smem, cudaStream_t s) {
-  if (smem > 40 * 1024) {  // with the kernels' own 4 KB more than the default 48 KB
+  if (smem > 40 * 1024) {  // with the kernels' own 6 KB more than the default 48 KB
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }

@@ -57,3 +57,29 @@ def test_rows_whose_squares_are_subnormal(time, D, dtype):
         for name, got, (v, b) in ((side + "_out", o, want["out"]), ("d" + side, g["d" + side], want["d"]),
                                   ("d%s_weight" % side, g["d%s_weight" % side], want["dw"])):
             ref.check(name, got, v, b + ref.EPS * v.abs() + 1e-37)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("time,D", [(False, 64), (False, 33), (False, 80), (True, 16), (True, 33), (True, 200)])
+def test_frequencies_that_are_no_numbers(time, D, interleaved, dtype):
+    """A NaN or infinite frequency makes its pair's elements NaN, both ways, and leaves the others' bits as they are."""
+    t = inputs(2, 24, 2, 1, D, dtype, time, seed=D)
+    rot = D // 2 * 2
+    f = freq(rot)
+    kw = dict(positions=t["positions"], interleaved=interleaved, layout="bhdl" if time else "blhd", norm=False)
+    axis = 2 if time else 3
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        j = rot // 4
+        e = f.clone()
+        e[j] = bad
+        pair = [2 * j, 2 * j + 1] if interleaved else [j, j + rot // 2]
+        rest = torch.tensor([n for n in range(D) if n not in pair], device="cuda")
+        pair = torch.tensor(pair, device="cuda")
+        results = []
+        for inv_freq in (f, e.double() if bad > 0 else e):
+            g = ssm.ssm_qk_norm_rope_bwd(t["dq_out"], t["q"], t["dk_out"], t["k"], inv_freq=inv_freq, **kw)
+            results.append(list(ssm.ssm_qk_norm_rope_fwd(t["q"], t["k"], inv_freq=inv_freq, **kw)) + [g["dq"], g["dk"]])
+        for good, got in zip(*results):
+            assert bool(got.index_select(axis, pair).isnan().all())
+            assert torch.equal(got.index_select(axis, rest), good.index_select(axis, rest))
