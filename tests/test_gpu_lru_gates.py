@@ -63,3 +63,31 @@ def test_channels_that_forget_at_once(Bt, Dn, L, packed, dtype):
     t["lam"] = torch.linspace(-3.0, 7.5, Dn).cuda()
     t["r_bias"] = torch.linspace(-2.0, 4.0, Dn).flip(0).roll(Dn // 3).cuda()
     run_and_check(t, ("r_bias", "i_bias", "h0") + (("reset", "lengths") if packed else ()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("Bt,Dn,L", SIZES)
+def test_nan_stays_in_a_sequence_that_forgets(Bt, Dn, L, dtype):
+    """Factors that underflow are no cuts: a NaN reaches the end of its own packed sequence forwards, and its start backwards, and no
+    further, whether or not a sequence starts in the same chunk."""
+    t = inputs(Bt, Dn, L, dtype, seed=L)
+    t["lam"] = torch.linspace(-1.0, 7.0, Dn).cuda()
+    t["r_bias"] = torch.full((Dn,), 2.0, device="cuda")
+    starts = sorted({0, L // 7, L // 7 + 3, L // 2, L // 2 + 1, L - 2})
+    reset = torch.zeros(Bt, L, dtype=torch.bool, device="cuda")
+    reset[:, starts] = True
+    args = lambda x: (x, t["r"], t["i"], t["lam"], t["r_bias"])  # noqa: E731
+    clean = ssm.ssm_lru_fwd(*args(t["x"]), reset=reset, save_states=True)
+    g0 = ssm.ssm_lru_bwd(t["dout"], *args(t["x"]), reset=reset, chunk_states=clean["chunk_states"])
+    step = torch.arange(L, device="cuda")
+    for lo, hi in zip(starts, starts[1:] + [L]):
+        for at in {lo, (lo + hi) // 2, hi - 1}:
+            x, d = t["x"].clone(), t["dout"].clone()
+            x[..., at] = d[..., at] = float("nan")
+            out = ssm.ssm_lru_fwd(*args(x), reset=reset)
+            ours = (step >= at) & (step < hi)
+            assert bool(out[..., ours].isnan().all()) and torch.equal(out[..., ~ours], clean["out"][..., ~ours]), (lo, hi, at)
+            g = ssm.ssm_lru_bwd(d, *args(t["x"]), reset=reset, chunk_states=clean["chunk_states"])
+            ours = (step >= lo) & (step <= at)
+            for k in ("dx", "di", "dr"):
+                assert bool(g[k][..., ours].isnan().all()) and torch.equal(g[k][..., ~ours], g0[k][..., ~ours]), (k, lo, hi, at)
