@@ -184,6 +184,10 @@ def marshal():
         except ImportError as e:
             raise ImportError("_marshal.so is not built or does not match this torch (%s); run "
                               "`python -m selective_state_space_34_b200.build`" % e) from e
+        from .build import built_for
+        if _marshal.BUILT_FOR != built_for():
+            raise ImportError("_marshal.so is built for %s, this is %s; run `python -m selective_state_space_34_b200.build`"
+                              % (_marshal.BUILT_FOR, built_for()))
         _native = _marshal
     return _native
 

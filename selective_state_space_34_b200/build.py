@@ -56,9 +56,21 @@ def _marshal_deps():
     return [os.path.join(CSRC, "ssm_marshal.cpp"), os.path.join(ROOT, "include", "ssm_scan.h")]
 
 
+def built_for() -> str:
+    """The torch and the Python that _marshal.so is compiled against; the module carries it as BUILT_FOR."""
+    import torch
+
+    return "torch %s, %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
+def _marshal_matches() -> bool:
+    with open(MARSHAL, "rb") as f:
+        return built_for().encode() + b"\0" in f.read()
+
+
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """Compile _marshal.so: plain C++ (no device code), linked to the library beside it and to torch."""
-    if not force and _newer(MARSHAL, _marshal_deps()):
+    if not force and _newer(MARSHAL, _marshal_deps()) and _marshal_matches():
         return MARSHAL
     import torch
 
@@ -67,7 +79,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
     tmp = MARSHAL + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), '-DSSM_BUILT_FOR="%s"' % built_for(),
            "-I" + sysconfig.get_paths()["include"], "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
            "-I" + os.path.join(cuda, "include"), os.path.join(CSRC, "ssm_marshal.cpp"), "-o", tmp,
            "-L" + PKG, "-l:libssm_scan.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch_dir, "lib"),
