@@ -386,10 +386,12 @@ ssm_status ssm_conv1d_silu(const void *x, void *u, const float *w, const float *
  *   a_t = exp(-c softplus(lam[d]) r_t)
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) g_t x_t,   h_{-1} = h0 or 0,   out_t = h_t
  *
- * x, r~ and i~ are given (the gates' projections are the caller's). State and sums are fp32. A layer
- * runs the causal conv of this library in front of it.
- *  - reset marks steps that start a new sequence (packed rows): h_{t-1} counts as 0 there, and
- *    nothing of an earlier sequence reaches a later one, NaN and infinity included, in either direction.
+ * x, r~ and i~ are given (the gates' projections are the caller's, and so is the causal conv that layers have in
+ * front: theirs has no SiLU, which ssm_conv1d_silu always applies). State and sums are fp32. A gate's
+ * argument below about -42 counts as -42: a gate is never below 2^-63.
+ *  - reset marks steps that start a new sequence (packed rows): h_{t-1} counts as 0 there (the input keeps its
+ *    factor sqrt(1 - a_t^2)), and nothing of an earlier sequence reaches a later one, NaN and infinity
+ *    included, in either direction.
  *  - lengths gives each batch element's live steps, 0 .. L (larger values count as L, negative ones as 0): out and the gradients are 0 behind
  *    them, whatever the inputs hold there, and h_last is the state after the last live step (h0
  *    with none).
@@ -473,7 +475,10 @@ ssm_status ssm_lru_step(const ssm_lru_step_args *args, void *stream);
  *   (2 j, 2 j + 1) with interleaved = 1:
  *     (n_p, n_q) -> rot_scale (n_p cos - n_q sin, n_q cos + n_p sin),  angle = position * inv_freq[j]
  *   the elements from rot on pass as they are.
- * The angle and its reduction are computed in 64 bits: an angle of x radians is off by about x 2^-53.
+ * The angle and its reduction are computed in 64 bits: an angle of x radians is off by up to x 2^-52, by 1.5e-9 (32 bits of a
+ * turn are kept, rounded down) and, once reduced, by 2^-24 of itself. fp32 inputs then take an accurate cosine and sine; bf16 inputs
+ * the hardware's, off by up to 2^-21, whatever the type of their outputs and gradients. A NaN or infinite inv_freq makes its
+ * pairs NaN.
  *
  * Element (b, t, h, e) of a tensor lies at b sb + h sh + t sr + e (layout SSM_QK_STATE_LAST), or
  * b sb + h sh + e sr + t (SSM_QK_TIME_LAST); strides count elements. Inputs may have any strides

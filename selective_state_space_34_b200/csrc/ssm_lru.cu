@@ -29,14 +29,11 @@
 // Precision. The decay goes through n = 1 - a (a polynomial for small |la|): 1 - a^2 = n + n a keeps its relative
 // precision where a is near 1, which a itself in 32 bits does not. States, sums and gradients are fp32 up to their one
 // rounding into the output's type; sigmoid, exp2 and the root are the hardware's (1 to 4 units of 2^-24), for
-// fp32 inputs too: against float64 the fp32 outputs are off by 2e-7 to 3e-7.
+// fp32 inputs too: against float64 the fp32 outputs and gradients of 3 x 1001 x 2047 are off by 3e-7 together.
 //
-// What bounds it. HBM, at 80% of the measured copy rate on long rows (bf16, 1 x 5120 x 65536 forward: 493 us, 5.4 TB/s;
-// 4 x 4096 x 4096 forward 100 us and backward 165 us of 82 and 143 us): 38 issue slots per element forwards and 58 backwards
-// are 72% and 65% of the SMs' issue, the four MUFU operations per element 60% of theirs forwards. What got it there:
-// packed fp32 pairs (59 -> 43 slots), 32-bit step counts and one branch around whole chunks (43 -> 37; 611 -> 552 us), the
-// fitted polynomial and the folded root (552 -> 500 us), cp.async rings for the backward (326 -> 290 us with the
-// forward), one warp per CTA (283 -> 267 us).
+// What bounds it. HBM, at 82% of the measured copy rate on long rows in a burst (bf16, 1 x 5120 x 65536 forward: 498 us, 5.4 TB/s; 534 to
+// 568 us call after call, when the chip is warm; 4 x 4096 x 4096 forward and backward 270 us of 225): 38 issue slots per element
+// forwards and 58 backwards are 72% and 65% of the SMs' issue, the four MUFU operations per element 60% of theirs forwards.
 #include <type_traits>
 
 #include "ssm_internal.h"

@@ -21,14 +21,15 @@
 //
 // Angles. In 32 bits position * inv_freq loses the angle of a far position (at 10^6 the spacing is 1/16 of
 // a radian). A frequency is kept as turns per position in units of 2^-64, so that the product with the position modulo 2^64 is
-// the reduced angle, exact but for the frequency's rounding in 64 bits (an angle of x radians is off by about x 2^-53);
-// what is left goes through the hardware sine (absolute error 2^-21) for bf16, sincospif for fp32 inputs.
+// the reduced angle, exact but for the frequency's roundings in 64 bits (an angle of x radians is off by x 2^-52 at most); the upper 32
+// bits of that (rounded down: 1.5e-9 radians), in fp32, go through the hardware sine (absolute error 2^-21) for bf16, sincospif for fp32
+// inputs.
 //
 // What bounds it. HBM by its bytes; in fact issue and the latency of a row's chain together (60% and 56% of the slots, 13 a element
 // forwards and 23 backwards, of which the angles are 1 to 6 by the number of heads that share them). 2 x 4096 tokens x 40 heads x 128,
-// bf16: forward 34 us (4.9 TB/s), backward 54 us (4.7 TB/s), with direct loads of four rows a step 64 and 112 us. Time innermost,
-// 8 x 65536 steps x 16 components, queries and keys, forward and backward: 71 us, without the ring, from L1, 116 us;
-// 4 x 8192 steps x 3 heads of 128: 59 us, by one warp for all pairs, in two passes from L1, 126 us.
+// bf16: forward and backward 88 us (4.8 TB/s for both calls' bytes), with direct loads of four rows a step 176 us. Time innermost,
+// 8 x 65536 steps x 16 components, queries and keys, bf16 gradients, forward and backward: 62 us (fp32 gradients 71, without the ring, from L1,
+// 116); 4 x 8192 steps x 3 heads of 128: 55 us (59, and by one warp for all pairs, in two passes from L1, 126).
 #include <type_traits>
 
 #include "ssm_internal.h"
@@ -223,7 +224,7 @@ template <typename... P> __device__ __forceinline__ bool advance(Walk &w, int H,
 }
 // Sums over the G lanes of a row.
 template <typename... F> __device__ __forceinline__ void sum_lanes(int G, F &...v) {
-  if (G == 8) {  // heads of 128
+  if (G == 8) {  // heads of 65 to 128 elements, mostly
 #pragma unroll
     for (int off = 4; off >= 1; off >>= 1) ((v += __shfl_xor_sync(kFull, v, off)), ...);
   } else {

@@ -33,7 +33,8 @@ def ssm_lru_fwd(x, r, i, lam, r_bias=None, i_bias=None, c: float = 8.0, h0=None,
     their sigmoids; lam, r_bias, i_bias: (Dn,) fp32; h0: (Bt, Dn) fp32. ``reset`` ((Bt, L) bool or uint8) marks
     the steps that start a new sequence, ``lengths`` ((Bt,) int32) the live steps of each batch element (behind
     them out is 0). Returns ``out`` (every h_t), or a dict with ``out`` and, when asked, ``chunk_states`` (for
-    ssm_lru_bwd) and ``h_last`` ((Bt, Dn) fp32, the state after the last live step)."""
+    ssm_lru_bwd) and ``h_last`` ((Bt, Dn) fp32, the state after the last live step). ``out``: a tensor to write
+    to, no input's memory."""
     return _abi.marshal().lru_fwd(x, r, i, lam, r_bias, i_bias, c, h0, reset, lengths, out_dtype, save_states, return_state,
                                   out)
 
@@ -111,8 +112,8 @@ def ssm_qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, inv_freq=None,
     slices of one projection need no copy. ``inv_freq`` ((rot / 2,) fp32 or fp64, see ssm_rope_inv_freq): the
     first rot elements of a head turn by position * inv_freq[j] in pairs (j, j + rot / 2), or (2 j, 2 j + 1) with
     ``interleaved``; cosine and sine are multiplied by ``rot_scale``. An ``eps`` below 2^-126 counts as 2^-126. ``positions``:
-    (Bt, L) int32 or int64, or None for pos0 + t. ``out``: (q_out, k_out) to write to, possibly q and k themselves (None in a place:
-    allocated). Returns (q_out, k_out)."""
+    (Bt, L) int32 or int64, or None for pos0 + t. ``out``: (q_out, k_out) to write to, q and k themselves or no
+    input's memory (None in a place: allocated). Returns (q_out, k_out)."""
     q_out, k_out = (None, None) if out is None else out
     return _abi.marshal().qk_fwd(q, k, q_weight, k_weight, inv_freq, positions, pos0, norm, eps, interleaved, rot_scale,
                                  _layout(layout), out_dtype, q_out, k_out)
