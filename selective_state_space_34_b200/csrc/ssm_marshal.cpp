@@ -388,9 +388,9 @@ PyObject *pair(PyObject *a, PyObject *b) {
   if (!t) throw python_error();
   return t;
 }
-PyObject *none() {
-  Py_INCREF(Py_None);
-  return Py_None;
+PyObject *held(PyObject *o) {
+  Py_INCREF(o);
+  return o;
 }
 
 // + out_dtype q_out k_out
@@ -399,19 +399,16 @@ PyObject *qk_fwd(PyObject *const *v) {
   const QkShapes r = qk_args(v, a);
   const ScalarType od = out_type("out_dtype", v[12], r.q.act);
   a.out_dtype = code("out_dtype", od);
-  PyObject *qo = v[13], *ko = v[14];
-  if (qo == Py_None) qo = wrap(r.q.empty(r.q.t.sizes(), od));
-  else Py_INCREF(qo);
-  if (!r.keys) ko = none();
-  else if (ko == Py_None) ko = wrap(r.q.empty(r.k, od));
-  else Py_INCREF(ko);
-  try {
+  PyObject *qo = nullptr, *ko = nullptr;
+  try {  // any of these may throw, an allocation without room too
+    qo = v[13] == Py_None ? wrap(r.q.empty(r.q.t.sizes(), od)) : held(v[13]);
+    ko = r.keys && v[14] == Py_None ? wrap(r.q.empty(r.k, od)) : held(r.keys ? v[14] : Py_None);
     SSM_PUT_HEADS(a, q_out, heads(r.q, "q_out", qo, od, r.q.t.sizes(), r.time));
     if (r.keys) SSM_PUT_HEADS(a, k_out, heads(r.q, "k_out", ko, od, r.k, r.time));
     run("ssm_qk_norm_rope_fwd", ssm_qk_norm_rope_fwd, a, r.q.dev);
   } catch (...) {
-    Py_DECREF(qo);
-    Py_DECREF(ko);
+    Py_XDECREF(qo);
+    Py_XDECREF(ko);
     throw;
   }
   return pair(qo, ko);

@@ -83,3 +83,16 @@ def test_frequencies_that_are_no_numbers(time, D, interleaved, dtype):
         for good, got in zip(*results):
             assert bool(got.index_select(axis, pair).isnan().all())
             assert torch.equal(got.index_select(axis, rest), good.index_select(axis, rest))
+
+
+def test_outputs_without_room_leave_no_memory_behind():
+    """The keys' output does not fit the device: the call fails as torch's allocations do, and the queries' output, made before, is freed."""
+    q = torch.zeros(1, 1 << 16, 1, 64, dtype=BF, device="cuda")
+    k = q[:, :, :1].expand(1, 1 << 16, 1 << 20, 64)  # 8 TiB of results
+    with pytest.raises(torch.OutOfMemoryError):
+        ssm.ssm_qk_norm_rope_fwd(q, k, inv_freq=freq(64))
+    before = torch.cuda.memory_allocated()
+    for _ in range(3):
+        with pytest.raises(torch.OutOfMemoryError):
+            ssm.ssm_qk_norm_rope_fwd(q, k, inv_freq=freq(64))
+    assert torch.cuda.memory_allocated() == before
